@@ -338,6 +338,97 @@ LQ_API lq_status lq_copy_slots(const lq_config *cfg, void *dst, int dst_num_slot
                                const int32_t *dst_slots, const void *src, int src_num_slots,
                                const int32_t *src_slots, int n, lq_stream_t stream);
 
+/* ---- Linear attention with one decay per head --------------------------
+ * A layer without the delta rule: per head
+ *     S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,
+ * over the FP32 blobs of a bits = 32 configuration with decay_kind 0 (others:
+ * LQ_ERR_UNSUPPORTED), so lq_state_init, lq_copy_slots, lq_dequant_state and
+ * lq_check_status work on the same buffers.
+ *   qk_heads  Hk: queries and keys have Hk heads, H % Hk == 0, and value head
+ *             h reads query / key head h / (H / Hk)
+ *   decay     a, in [0, 1]; a negative, infinite or NaN gate sets LQ_DEV_RANGE
+ * Alignment: q, k, v, S0, out and workspace 16 bytes, decay, slots and
+ * lengths 4.  A non-finite q, k or v makes its head's state non-finite, as
+ * the formula has it; in a prompt it may also reach outputs of the same head
+ * up to 63 tokens before it. */
+
+/* One token for every (slot, head).
+ *   q, k [N, Hk, dk]  v [N, H, dv] in_dtype   decay [N, H]   out [N, H, dv] f32
+ * A (slot, head) whose status is nonzero or whose gate is bad is skipped: zero
+ * outputs, state unchanged. */
+LQ_API lq_status lq_linear_step(const lq_config *cfg, void *state, int qk_heads, const void *q, const void *k,
+                                const void *v, const float *decay, float *out, lq_stream_t stream);
+
+/* The same for the slots in `slots` (n_active rows in place of N; a row whose
+ * slot is out of range gets zero outputs). */
+LQ_API lq_status lq_linear_step_slots(const lq_config *cfg, void *state, const int32_t *slots, int n_active,
+                                      int qk_heads, const void *q, const void *k, const void *v, const float *decay,
+                                      float *out, lq_stream_t stream);
+
+/* Bytes of workspace with which lq_linear_prefill of `rows` rows of up to
+ * `tokens` tokens may cut its prompts along time (it does where the heads
+ * alone leave SMs idle); 0: not cut, no workspace needed.  Host only. */
+LQ_API size_t lq_linear_prefill_workspace(const lq_config *cfg, int rows, int tokens);
+
+/* A prompt for every (slot, head).
+ *   tokens   T >= 0
+ *   lengths  [N] int32, device, or NULL: row n's prompt is its first
+ *            clamp(lengths[n], 0, T) tokens; what lies behind is not read
+ *   S0       [N, H, dk, dv] f32 or NULL (zero state)
+ *   q, k     [N, T, Hk, dk]  v [N, T, H, dv] in_dtype   decay [N, T, H] f32
+ *   out      [N, T, H, dv] f32 or NULL; zero past a row's length
+ *   flags    LQ_PREFILL_CONTINUE: go on from the state in the blobs (S0 must
+ *            be NULL; a (slot, head) whose status is nonzero is skipped, with
+ *            zero outputs); without it the header is written anew
+ *   workspace, workspace_bytes: device memory of at least
+ *            lq_linear_prefill_workspace(cfg, N, T) bytes, or NULL (then the
+ *            prompt is not cut).  Its content is not kept; calls that may run
+ *            at the same time, graph replays too, need one each.
+ * A prompt ends before its first bad gate (LQ_DEV_RANGE; zero outputs from
+ * there on, the state holds the tokens before it). */
+#define LQ_PREFILL_CONTINUE 0x1u
+LQ_API lq_status lq_linear_prefill(const lq_config *cfg, void *state, int tokens, const int32_t *lengths,
+                                   const float *S0, int qk_heads, const void *q, const void *k, const void *v,
+                                   const float *decay, float *out, uint32_t flags, void *workspace,
+                                   size_t workspace_bytes, lq_stream_t stream);
+
+/* The same for the slots in `slots` (n_active rows in place of N). */
+LQ_API lq_status lq_linear_prefill_slots(const lq_config *cfg, void *state, const int32_t *slots, int n_active,
+                                         int tokens, const int32_t *lengths, const float *S0, int qk_heads,
+                                         const void *q, const void *k, const void *v, const float *decay, float *out,
+                                         uint32_t flags, void *workspace, size_t workspace_bytes,
+                                         lq_stream_t stream);
+
+/* ---- Norms and gates around the recurrence ----------------------------
+ * They take any valid configuration (its dk == dv, num_heads, decay_kind and
+ * in_dtype are used) and serve every decode and prefill call above. */
+
+/* Before the recurrence, for `rows` tokens (any [.., H, d] tensors with that
+ * many leading rows, so [N, T] too):
+ *   q_out = q_scale q / sqrt(sum q^2 + eps),  k_out = k / sqrt(sum k^2 + eps)
+ *   decay = exp(-exp(a_log_h) softplus(a + dt_bias)),  beta = 1 / (1 + exp(-b))
+ *   q, k, q_out, k_out [rows, Hk, dk] in_dtype (q_out may be q, k_out may be k)
+ *   a  [rows, H] in_dtype, dt_bias [H] f32, decay [rows, H] f32 (decay_kind 0);
+ *      [rows, H, dk], [H, dk] and [rows, H, dk] (decay_kind 1)
+ *   b  [rows, H] in_dtype, a_log [H] f32, beta [rows, H] f32
+ * Sums and gates in FP32, one rounding to in_dtype.  Alignment: q, k, q_out,
+ * k_out 16 bytes, with decay_kind 1 a, dt_bias and decay too; the rest their
+ * element size. */
+LQ_API lq_status lq_qk_norm(const lq_config *cfg, int rows, int qk_heads, const void *q, const void *k, const void *a,
+                            const void *b, const float *a_log, const float *dt_bias, float q_scale, float eps,
+                            void *q_out, void *k_out, float *decay, float *beta, lq_stream_t stream);
+
+/* After it, from the FP32 rows that every call above writes:
+ *   y = o / sqrt(mean o^2 + eps) * weight * act(gate)
+ *   o [rows, H, dv] f32, weight [dv] f32 or NULL (ones), gate and y
+ *   [rows, H, dv] in_dtype; gate is NULL for LQ_GATE_NONE and only then.
+ * FP32 throughout, one rounding to in_dtype.  Alignment 16 bytes. */
+#define LQ_GATE_NONE 0
+#define LQ_GATE_SILU 1
+#define LQ_GATE_SIGMOID 2
+LQ_API lq_status lq_out_norm(const lq_config *cfg, int rows, const float *o, const float *weight, const void *gate,
+                             int gate_kind, float eps, void *y, lq_stream_t stream);
+
 /* Diagnostic of the device-side failure detection: one kernel thread waits,
  * through the bounded wait every kernel of this library uses, on an on-chip
  * barrier that nothing ever arrives on.  The wait gives up after its time

@@ -24,6 +24,8 @@ ENTRY_POINTS = ("lq_validate_config", "lq_state_bytes", "lq_state_init", "lq_dec
                 "lq_decode_steps", "lq_window_flush", "lq_dequant_state", "lq_check_status",
                 "lq_prefill", "lq_state_init_slots", "lq_decode_step_slots", "lq_decode_steps_slots",
                 "lq_window_flush_slots", "lq_prefill_slots", "lq_copy_slots", "lq_selftest_wait",
+                "lq_linear_step", "lq_linear_step_slots", "lq_linear_prefill_workspace", "lq_linear_prefill",
+                "lq_linear_prefill_slots", "lq_qk_norm", "lq_out_norm",
                 "lq_status_string")
 
 
@@ -100,6 +102,21 @@ def _load():
     L.lq_prefill_slots.argtypes = [P, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.lq_prefill_slots.restype = st
     L.lq_copy_slots.restype = st
+    f32, u32, sz = ctypes.c_float, ctypes.c_uint32, ctypes.c_size_t
+    L.lq_linear_step.argtypes = [P, vp, i32, vp, vp, vp, vp, vp, vp]
+    L.lq_linear_step.restype = st
+    L.lq_linear_step_slots.argtypes = [P, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.lq_linear_step_slots.restype = st
+    L.lq_linear_prefill_workspace.argtypes = [P, i32, i32]
+    L.lq_linear_prefill_workspace.restype = sz
+    L.lq_linear_prefill.argtypes = [P, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, u32, vp, sz, vp]
+    L.lq_linear_prefill.restype = st
+    L.lq_linear_prefill_slots.argtypes = [P, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, u32, vp, sz, vp]
+    L.lq_linear_prefill_slots.restype = st
+    L.lq_qk_norm.argtypes = [P, i32, i32, vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
+    L.lq_qk_norm.restype = st
+    L.lq_out_norm.argtypes = [P, i32, vp, vp, vp, i32, f32, vp, vp]
+    L.lq_out_norm.restype = st
     L.lq_selftest_wait.argtypes = [vp, vp]
     L.lq_selftest_wait.restype = st
     L.lq_status_string.argtypes = [st]
@@ -330,6 +347,138 @@ def lq_copy_slots(cfg, dst, dst_num_slots, dst_slots, src, src_num_slots, src_sl
                              _stream(stream)), "lq_copy_slots")
 
 
+# ---- linear attention with one decay per head ------------------------------
+
+def _linear_specs(cfg, rows, T, qk_heads, q, k, v, decay, out):
+    Hk = cfg.num_heads if qk_heads is None else int(qk_heads)
+    n, m = rows * T * cfg.num_heads, rows * T * Hk
+    return Hk, [_spec(q, "q", _in_dt(cfg), m * cfg.dk), _spec(k, "k", _in_dt(cfg), m * cfg.dk),
+                _spec(v, "v", _in_dt(cfg), n * cfg.dv), _spec(decay, "decay", "f32", n),
+                _spec(out, "out", "f32", n * cfg.dv)]
+
+
+def lq_linear_step(cfg, state, q, k, v, decay, out, qk_heads=None, stream=None):
+    """One token: S = a S + k v^T, out = S^T q.  qk_heads: heads of q and k (default: as many as v)."""
+    Hk, specs = _linear_specs(cfg, cfg.num_slots, 1, qk_heads, q, k, v, decay, out)
+    _validate(_state_spec(cfg, state), *specs)
+    _check(lib.lq_linear_step(ctypes.byref(cfg), _ptr(state), Hk, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(out),
+                              _stream(stream)), "lq_linear_step")
+
+
+def lq_linear_step_slots(cfg, state, slots, q, k, v, decay, out, qk_heads=None, stream=None):
+    Hk, specs = _linear_specs(cfg, _n(slots), 1, qk_heads, q, k, v, decay, out)
+    _validate(_state_spec(cfg, state), _spec(slots, "slots", "i32"), *specs)
+    _check(lib.lq_linear_step_slots(ctypes.byref(cfg), _ptr(state), _ptr(slots), _n(slots), Hk, _ptr(q), _ptr(k),
+                                    _ptr(v), _ptr(decay), _ptr(out), _stream(stream)), "lq_linear_step_slots")
+
+
+LQ_PREFILL_CONTINUE = 0x1
+
+
+def lq_linear_prefill_workspace(cfg, rows, tokens) -> int:
+    return lib.lq_linear_prefill_workspace(ctypes.byref(cfg), int(rows), int(tokens))
+
+
+def _torch_stream(stream):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream()
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return stream
+
+
+def _linear_workspace(cfg, rows, tokens, workspace, stream):
+    """The workspace of a prefill call: the caller's, or memory of the caching
+    allocator, taken on the call's stream and given back to it, in stream
+    order, when the call has been enqueued (inside a graph capture: memory of
+    that graph's pool)."""
+    need = lq_linear_prefill_workspace(cfg, rows, tokens) if rows > 0 else 0
+    if workspace is not None or not need:
+        return workspace, need
+    import torch
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.empty(need, dtype=torch.uint8, device="cuda"), need
+
+
+def _ws_bytes(workspace, need):
+    """Raw addresses are vouched for by their owner."""
+    if workspace is None:
+        return 0
+    return need if isinstance(workspace, int) else workspace.numel()
+
+
+def lq_linear_prefill(cfg, state, tokens, q, k, v, decay, S0=None, lengths=None, out=None, qk_heads=None,
+                      cont=False, workspace=None, stream=None):
+    """A prompt of T tokens per (slot, head), inputs [N, T, H, .].  cont: go on
+    from the state in the blobs.  workspace: a uint8 tensor of
+    lq_linear_prefill_workspace(cfg, N, T) bytes; allocated here when None."""
+    T, rows = max(int(tokens), 0), cfg.num_slots
+    Hk, specs = _linear_specs(cfg, rows, T, qk_heads, q, k, v, decay, out)
+    _validate(_state_spec(cfg, state), *specs, _dense_spec(cfg, S0, "S0", rows), _spec(lengths, "lengths", "i32", rows),
+              _spec(workspace, "workspace", "u8"))
+    ws, need = _linear_workspace(cfg, rows, T, workspace, stream)
+    _check(lib.lq_linear_prefill(ctypes.byref(cfg), _ptr(state), int(tokens), _ptr(lengths), _ptr(S0), Hk, _ptr(q),
+                                 _ptr(k), _ptr(v), _ptr(decay), _ptr(out), LQ_PREFILL_CONTINUE if cont else 0,
+                                 _ptr(ws), _ws_bytes(ws, need), _stream(stream)), "lq_linear_prefill")
+
+
+def lq_linear_prefill_slots(cfg, state, slots, tokens, q, k, v, decay, S0=None, lengths=None, out=None,
+                            qk_heads=None, cont=False, workspace=None, stream=None):
+    T, rows = max(int(tokens), 0), _n(slots)
+    Hk, specs = _linear_specs(cfg, rows, T, qk_heads, q, k, v, decay, out)
+    _validate(_state_spec(cfg, state), _spec(slots, "slots", "i32"), *specs, _dense_spec(cfg, S0, "S0", rows),
+              _spec(lengths, "lengths", "i32", rows), _spec(workspace, "workspace", "u8"))
+    ws, need = _linear_workspace(cfg, rows, T, workspace, stream)
+    _check(lib.lq_linear_prefill_slots(ctypes.byref(cfg), _ptr(state), _ptr(slots), rows, int(tokens), _ptr(lengths),
+                                       _ptr(S0), Hk, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(out),
+                                       LQ_PREFILL_CONTINUE if cont else 0, _ptr(ws), _ws_bytes(ws, need),
+                                       _stream(stream)), "lq_linear_prefill_slots")
+
+
+# ---- norms and gates around the recurrence ---------------------------------
+
+GATE_KINDS = {"none": 0, "silu": 1, "sigmoid": 2}
+
+
+def _rows(x, per, what, rows):
+    if rows is not None:
+        return int(rows)
+    if isinstance(x, int):
+        raise ValueError(f"rows is needed where {what} is an address")
+    if per <= 0 or x.numel() % per:
+        raise ValueError(f"{what}: {x.numel()} elements, not a multiple of {per}")
+    return x.numel() // per
+
+
+def lq_qk_norm(cfg, q, k, a, b, a_log, dt_bias, q_out, k_out, decay, beta, q_scale=1.0, eps=1e-6, qk_heads=None,
+               rows=None, stream=None):
+    """q and k rows to unit length (q times q_scale), decay and beta from their
+    logits, for any number of leading rows (default: those of q)."""
+    H = cfg.num_heads
+    Hk = H if qk_heads is None else int(qk_heads)
+    M = _rows(q, Hk * cfg.dk, "q", rows)
+    n, ch, dt = M * H, (cfg.dk if cfg.decay_kind == 1 else 1), _in_dt(cfg)
+    _validate(*[_spec(x, w, dt, M * Hk * cfg.dk) for x, w in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))],
+              _spec(a, "a", dt, n * ch), _spec(b, "b", dt, n), _spec(a_log, "a_log", "f32", H),
+              _spec(dt_bias, "dt_bias", "f32", H * ch), _spec(decay, "decay", "f32", n * ch), _spec(beta, "beta", "f32", n))
+    _check(lib.lq_qk_norm(ctypes.byref(cfg), M, Hk, _ptr(q), _ptr(k), _ptr(a), _ptr(b), _ptr(a_log), _ptr(dt_bias),
+                          float(q_scale), float(eps), _ptr(q_out), _ptr(k_out), _ptr(decay), _ptr(beta),
+                          _stream(stream)), "lq_qk_norm")
+
+
+def lq_out_norm(cfg, o, y, weight=None, gate=None, gate_kind="none", eps=1e-6, rows=None, stream=None):
+    """y = o / sqrt(mean o^2 + eps) * weight * act(gate); gate_kind "none", "silu" or "sigmoid"."""
+    if gate_kind not in GATE_KINDS:
+        raise ValueError(f"gate_kind {gate_kind!r}, expected one of {', '.join(GATE_KINDS)}")
+    M = _rows(o, cfg.num_heads * cfg.dv, "o", rows)
+    n = M * cfg.num_heads * cfg.dv
+    _validate(_spec(o, "o", "f32", n), _spec(y, "y", _in_dt(cfg), n), _spec(weight, "weight", "f32", cfg.dv),
+              _spec(gate, "gate", _in_dt(cfg), n))
+    _check(lib.lq_out_norm(ctypes.byref(cfg), M, _ptr(o), _ptr(weight), _ptr(gate), GATE_KINDS[gate_kind], float(eps),
+                           _ptr(y), _stream(stream)), "lq_out_norm")
+
+
 def lq_selftest_wait(status, stream=None):
     """Device diagnostic: a bounded wait that runs out writes LQ_DEV_TIMEOUT to status."""
     _validate(_spec(status, "status", "i32", 1, at_least=True))
@@ -337,14 +486,16 @@ def lq_selftest_wait(status, stream=None):
 
 
 class LQState:
-    """N*H state blobs in one device buffer, with the library's calls bound."""
+    """N*H state blobs in one device buffer (allocated here, or `buf`), with
+    the library's calls bound."""
 
-    def __init__(self, cfg: lq_config, device="cuda"):
-        import torch
+    def __init__(self, cfg: lq_config, device="cuda", buf=None):
         self.cfg = cfg
         self.blob_bytes = lq_state_bytes(cfg)
-        self.buf = torch.empty(cfg.num_slots * cfg.num_heads * self.blob_bytes, dtype=torch.uint8,
-                               device=device)
+        if buf is None:
+            import torch
+            buf = torch.empty(cfg.num_slots * cfg.num_heads * self.blob_bytes, dtype=torch.uint8, device=device)
+        self.buf = buf
 
     @property
     def ptr(self) -> int:
@@ -399,3 +550,21 @@ class LQState:
 
     def flush_slots(self, slots, stream=None):
         lq_window_flush_slots(self.cfg, self.buf, slots, stream)
+
+    # linear attention with one decay per head (bits = 32)
+    def linear_step(self, q, k, v, decay, out, qk_heads=None, stream=None):
+        lq_linear_step(self.cfg, self.buf, q, k, v, decay, out, qk_heads, stream)
+
+    def linear_step_slots(self, slots, q, k, v, decay, out, qk_heads=None, stream=None):
+        lq_linear_step_slots(self.cfg, self.buf, slots, q, k, v, decay, out, qk_heads, stream)
+
+    def linear_prefill(self, tokens, q, k, v, decay, S0=None, lengths=None, out=None, qk_heads=None, cont=False,
+                       workspace=None, stream=None):
+        """Prompt of T tokens per (slot, head) (inputs [N, T, H, .]); cont: go on from the state."""
+        lq_linear_prefill(self.cfg, self.buf, tokens, q, k, v, decay, S0, lengths, out, qk_heads, cont, workspace,
+                          stream)
+
+    def linear_prefill_slots(self, slots, tokens, q, k, v, decay, S0=None, lengths=None, out=None, qk_heads=None,
+                             cont=False, workspace=None, stream=None):
+        lq_linear_prefill_slots(self.cfg, self.buf, slots, tokens, q, k, v, decay, S0, lengths, out, qk_heads, cont,
+                                workspace, stream)

@@ -1,0 +1,293 @@
+// linear.cu -- host side of the linear-attention entry points of
+// include/leapquant.h: argument checks and launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "leapquant.h"
+#include "lq_common.cuh"
+#include "lq_host.cuh"
+#include "lq_linear.cuh"
+#include "lq_norms.cuh"
+
+using namespace lq;
+
+namespace {
+
+constexpr int kSms = 148;
+
+// A prompt is cut along time where its heads alone leave most SMs idle; a
+// segment has at least kMinSegment tokens.
+constexpr int kMinSegment = 256;
+constexpr int kMaxSegments = 64;
+
+struct Cut {
+    int seg_len, nseg;
+};
+
+Cut cut_of(int64_t work, int tokens) {
+    Cut c{tokens > 0 ? tokens : 1, 1};
+    if (work <= 0 || work >= kSms || tokens < 2 * kMinSegment) return c;
+    int64_t n = (2 * kSms) / work;
+    if (n > tokens / kMinSegment) n = tokens / kMinSegment;
+    if (n > kMaxSegments) n = kMaxSegments;
+    if (n < 2) return c;
+    c.seg_len = (int)align_up((uint32_t)((tokens + n - 1) / n), 64u);
+    c.nseg = (tokens + c.seg_len - 1) / c.seg_len;
+    return c;
+}
+
+// [work, nseg, dk, dv] f32 states | [work, nseg] gate products | [work, nseg]
+// first bad tokens | [work] run flags
+size_t workspace_bytes(const lq_config &c, int64_t work, const Cut &cut) {
+    if (cut.nseg < 2) return 0;
+    const size_t n = (size_t)work * cut.nseg;
+    return (n * ((size_t)c.dk * c.dv + 2) + (size_t)work) * 4u;
+}
+
+lq_status check_linear(const lq_config *cfg, int qk_heads) {
+    const lq_status st = check_config(cfg);
+    if (st != LQ_OK) return st;
+    if (qk_heads <= 0 || cfg->num_heads % qk_heads != 0) return LQ_ERR_INVALID_ARG;
+    if (cfg->bits != 32 || cfg->decay_kind != 0) return LQ_ERR_UNSUPPORTED;
+    return LQ_OK;
+}
+
+template <typename... KArgs>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster, uint32_t smem, cudaStream_t s,
+                           LinArgs a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int D, bool BF16>
+lq_status launch_step(const LinArgs &a, cudaStream_t s) {
+    // few heads: four CTAs per head, so that every SM has loads in flight
+    if (a.work < 2 * kSms) return launched(launch_pdl(lin_step_kernel<D, BF16, D / 4>, a.work * 4, 256, 0u, s, a));
+    return launched(launch_pdl(lin_step_kernel<D, BF16, D>, a.work, 256, 0u, s, a));
+}
+
+lq_status step_rows(const lq_config &c, void *state, const int32_t *slots, int rows, int qk_heads, const void *q,
+                    const void *k, const void *v, const float *decay, float *out, lq_stream_t stream) {
+    if (rows > 0 && (!q || !k || !v || !decay || !out)) return LQ_ERR_INVALID_ARG;
+    if ((int64_t)rows * c.num_heads > 0x7FFFFFFF / 8) return LQ_ERR_UNSUPPORTED;
+    if (!aligned(state, 256) || !aligned(slots, 4) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(decay, 4) || !aligned(out, 16))
+        return LQ_ERR_MISALIGNED;
+    if (rows == 0) return LQ_OK;
+    LinArgs a{};
+    a.state = static_cast<uint8_t *>(state);
+    a.L = make_layout(c);
+    a.map = SlotMap{slots, c.num_heads, c.num_slots};
+    a.q = q; a.k = k; a.v = v; a.decay = decay; a.out = out;
+    a.tokens = 1;
+    a.work = rows * c.num_heads;
+    a.qk_heads = qk_heads;
+    a.group = c.num_heads / qk_heads;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c.dk == 128) return c.in_dtype ? launch_step<128, true>(a, s) : launch_step<128, false>(a, s);
+    return c.in_dtype ? launch_step<64, true>(a, s) : launch_step<64, false>(a, s);
+}
+
+template <int D, bool BF16, int C>
+lq_status launch_recurrent(const LinArgs &a, cudaStream_t s) {
+    using SH = LinShape<D, BF16, C>;
+    if (a.nseg > 1) {
+        auto k = lin_recurrent_kernel<D, BF16, C, true>;
+        if (allow_smem(k, SH::SMEM) != cudaSuccess) return LQ_ERR_CUDA;
+        if (launch_cluster(k, dim3((unsigned)(a.work * SH::NB), (unsigned)(a.nseg - 1)), kLinThreads, 1, SH::SMEM, s,
+                           a) != cudaSuccess)
+            return LQ_ERR_CUDA;
+        if (launch_pdl(lin_scan_kernel<D>, a.work * (D * D / 1024), 256, 0u, s, a) != cudaSuccess) return LQ_ERR_CUDA;
+    }
+    auto k = lin_recurrent_kernel<D, BF16, C, false>;
+    if (allow_smem(k, SH::SMEM) != cudaSuccess) return LQ_ERR_CUDA;
+    return launched(launch_cluster(k, dim3((unsigned)(a.work * SH::NB), (unsigned)a.nseg), kLinThreads, SH::NB,
+                                   SH::SMEM, s, a));
+}
+
+template <int D, bool BF16>
+lq_status launch_prefill(const LinArgs &a, cudaStream_t s) {
+    // few heads: 16 columns per CTA, else 64
+    if ((int64_t)a.work * a.nseg * (D / 64) < 2 * kSms) return launch_recurrent<D, BF16, 1>(a, s);
+    return launch_recurrent<D, BF16, 4>(a, s);
+}
+
+lq_status prefill_rows(const lq_config &c, void *state, const int32_t *slots, int rows, int tokens,
+                       const int32_t *lengths, const float *S0, int qk_heads, const void *q, const void *k,
+                       const void *v, const float *decay, float *out, uint32_t flags, void *workspace,
+                       size_t workspace_size, lq_stream_t stream) {
+    if (tokens < 0 || (flags & ~LQ_PREFILL_CONTINUE)) return LQ_ERR_INVALID_ARG;
+    if ((flags & LQ_PREFILL_CONTINUE) && S0) return LQ_ERR_INVALID_ARG;
+    if ((int64_t)rows * (tokens > 0 ? tokens : 1) * c.num_heads > 0x7FFFFFFF) return LQ_ERR_UNSUPPORTED;
+    if ((int64_t)rows * c.num_heads > 0x7FFFFFFF / 16) return LQ_ERR_UNSUPPORTED;
+    if (rows > 0 && tokens > 0 && (!q || !k || !v || !decay)) return LQ_ERR_INVALID_ARG;
+    if (!aligned(state, 256) || !aligned(slots, 4) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(decay, 4) || !aligned(out, 16) || !aligned(S0, 16) || !aligned(lengths, 4) || !aligned(workspace, 16))
+        return LQ_ERR_MISALIGNED;
+    if (rows == 0) return LQ_OK;
+    LinArgs a{};
+    a.state = static_cast<uint8_t *>(state);
+    a.L = make_layout(c);
+    a.map = SlotMap{slots, c.num_heads, c.num_slots};
+    a.S0 = S0;
+    a.q = q; a.k = k; a.v = v; a.decay = decay; a.lengths = lengths;
+    a.out = tokens > 0 ? out : nullptr;
+    a.tokens = tokens;
+    a.work = rows * c.num_heads;
+    a.qk_heads = qk_heads;
+    a.group = c.num_heads / qk_heads;
+    a.cont = (flags & LQ_PREFILL_CONTINUE) != 0u;
+    Cut cut = cut_of(a.work, tokens);
+    if (workspace) {
+        if (workspace_size < workspace_bytes(c, a.work, cut)) return LQ_ERR_INVALID_ARG;
+    } else {
+        cut = Cut{tokens > 0 ? tokens : 1, 1};
+    }
+    a.seg_len = cut.seg_len;
+    a.nseg = cut.nseg;
+    if (a.nseg > 1) {
+        const size_t n = (size_t)a.work * a.nseg;
+        a.ws_S = static_cast<float *>(workspace);
+        a.ws_g = a.ws_S + n * (size_t)(c.dk * c.dv);
+        a.ws_bad = reinterpret_cast<int *>(a.ws_g + n);
+        a.ws_run = a.ws_bad + n;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c.dk == 128) return c.in_dtype ? launch_prefill<128, true>(a, s) : launch_prefill<128, false>(a, s);
+    return c.in_dtype ? launch_prefill<64, true>(a, s) : launch_prefill<64, false>(a, s);
+}
+
+lq_status check_linear_slots(const lq_config *cfg, const void *state, const int32_t *slots, int n_active,
+                             int qk_heads) {
+    const lq_status st = check_linear(cfg, qk_heads);
+    if (st != LQ_OK) return st;
+    if (!state || n_active < 0 || (n_active > 0 && !slots)) return LQ_ERR_INVALID_ARG;
+    return LQ_OK;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_qk_norm(QkNormArgs a, cudaStream_t s) {
+    constexpr int LR = D / (BF16 ? 8 : 4), per = 256 / LR * kNormUnroll;
+    const long long nb = (2 * a.qk_rows + per - 1) / per;
+    const long long gates = a.kda ? a.heads_n * LR : a.heads_n;
+    const long long ng = (gates + 255) / 256;
+    if (nb + ng > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    a.norm_blocks = (unsigned)nb;
+    return launch_pdl(qk_norm_kernel<D, BF16>, (int)(nb + ng), 256, 0u, s, a);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_out_norm(const OutNormArgs &a, int gate, cudaStream_t s) {
+    constexpr int per = 256 / (D / 8) * kOutNormUnroll;
+    const int grid = (int)((a.n + per - 1) / per);
+    switch (gate) {
+        case kGateNone: return launch_pdl(out_norm_kernel<D, BF16, kGateNone>, grid, 256, 0u, s, a);
+        case kGateSilu: return launch_pdl(out_norm_kernel<D, BF16, kGateSilu>, grid, 256, 0u, s, a);
+        default: return launch_pdl(out_norm_kernel<D, BF16, kGateSigmoid>, grid, 256, 0u, s, a);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+lq_status lq_linear_step(const lq_config *cfg, void *state, int qk_heads, const void *q, const void *k, const void *v,
+                         const float *decay, float *out, lq_stream_t stream) {
+    const lq_status st = check_linear(cfg, qk_heads);
+    if (st != LQ_OK) return st;
+    if (!state) return LQ_ERR_INVALID_ARG;
+    return step_rows(*cfg, state, nullptr, cfg->num_slots, qk_heads, q, k, v, decay, out, stream);
+}
+
+lq_status lq_linear_step_slots(const lq_config *cfg, void *state, const int32_t *slots, int n_active, int qk_heads,
+                               const void *q, const void *k, const void *v, const float *decay, float *out,
+                               lq_stream_t stream) {
+    const lq_status st = check_linear_slots(cfg, state, slots, n_active, qk_heads);
+    if (st != LQ_OK) return st;
+    return step_rows(*cfg, state, slots, n_active, qk_heads, q, k, v, decay, out, stream);
+}
+
+size_t lq_linear_prefill_workspace(const lq_config *cfg, int rows, int tokens) {
+    if (check_linear(cfg, 1) != LQ_OK || rows <= 0 || tokens <= 0) return 0;
+    const int64_t work = (int64_t)rows * cfg->num_heads;
+    return workspace_bytes(*cfg, work, cut_of(work, tokens));
+}
+
+lq_status lq_linear_prefill(const lq_config *cfg, void *state, int tokens, const int32_t *lengths, const float *S0,
+                            int qk_heads, const void *q, const void *k, const void *v, const float *decay, float *out,
+                            uint32_t flags, void *workspace, size_t workspace_bytes, lq_stream_t stream) {
+    const lq_status st = check_linear(cfg, qk_heads);
+    if (st != LQ_OK) return st;
+    if (!state) return LQ_ERR_INVALID_ARG;
+    return prefill_rows(*cfg, state, nullptr, cfg->num_slots, tokens, lengths, S0, qk_heads, q, k, v, decay, out, flags,
+                        workspace, workspace_bytes, stream);
+}
+
+lq_status lq_linear_prefill_slots(const lq_config *cfg, void *state, const int32_t *slots, int n_active, int tokens,
+                                  const int32_t *lengths, const float *S0, int qk_heads, const void *q, const void *k,
+                                  const void *v, const float *decay, float *out, uint32_t flags, void *workspace,
+                                  size_t workspace_bytes, lq_stream_t stream) {
+    const lq_status st = check_linear_slots(cfg, state, slots, n_active, qk_heads);
+    if (st != LQ_OK) return st;
+    return prefill_rows(*cfg, state, slots, n_active, tokens, lengths, S0, qk_heads, q, k, v, decay, out, flags,
+                        workspace, workspace_bytes, stream);
+}
+
+lq_status lq_qk_norm(const lq_config *cfg, int rows, int qk_heads, const void *q, const void *k, const void *a,
+                     const void *b, const float *a_log, const float *dt_bias, float q_scale, float eps, void *q_out,
+                     void *k_out, float *decay, float *beta, lq_stream_t stream) {
+    const lq_status st = check_config(cfg);
+    if (st != LQ_OK) return st;
+    if (rows < 0 || qk_heads <= 0 || cfg->num_heads % qk_heads != 0 || !(eps >= 0.f)) return LQ_ERR_INVALID_ARG;
+    if (rows > 0 && (!q || !k || !a || !b || !a_log || !dt_bias || !q_out || !k_out || !decay || !beta))
+        return LQ_ERR_INVALID_ARG;
+    const lq_config &c = *cfg;
+    if ((int64_t)rows * c.num_heads > 0x7FFFFFFF) return LQ_ERR_UNSUPPORTED;
+    const uintptr_t e = c.in_dtype ? 2 : 4;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+        !aligned(a, c.decay_kind ? 16 : e) || !aligned(b, e) || !aligned(a_log, 4) ||
+        !aligned(dt_bias, c.decay_kind ? 16 : 4) || !aligned(decay, c.decay_kind ? 16 : 4) || !aligned(beta, 4))
+        return LQ_ERR_MISALIGNED;
+    if (rows == 0) return LQ_OK;
+    QkNormArgs n{q, k, a, b, a_log, dt_bias, q_out, k_out, decay, beta, q_scale, eps, (long long)rows * qk_heads,
+                 (long long)rows * c.num_heads, c.num_heads, c.decay_kind, 0u};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c.dk == 128)
+        return launched(c.in_dtype ? launch_qk_norm<128, true>(n, s) : launch_qk_norm<128, false>(n, s));
+    return launched(c.in_dtype ? launch_qk_norm<64, true>(n, s) : launch_qk_norm<64, false>(n, s));
+}
+
+lq_status lq_out_norm(const lq_config *cfg, int rows, const float *o, const float *weight, const void *gate,
+                      int gate_kind, float eps, void *y, lq_stream_t stream) {
+    const lq_status st = check_config(cfg);
+    if (st != LQ_OK) return st;
+    if (rows < 0 || gate_kind < LQ_GATE_NONE || gate_kind > LQ_GATE_SIGMOID || !(eps >= 0.f)) return LQ_ERR_INVALID_ARG;
+    if ((gate_kind == LQ_GATE_NONE) != (gate == nullptr) && rows > 0) return LQ_ERR_INVALID_ARG;
+    if (rows > 0 && (!o || !y)) return LQ_ERR_INVALID_ARG;
+    const lq_config &c = *cfg;
+    if ((int64_t)rows * c.num_heads > 0x7FFFFFFF) return LQ_ERR_UNSUPPORTED;
+    if (!aligned(o, 16) || !aligned(weight, 16) || !aligned(gate, 16) || !aligned(y, 16)) return LQ_ERR_MISALIGNED;
+    if (rows == 0) return LQ_OK;
+    OutNormArgs n{o, weight, gate, y, eps, (long long)rows * c.num_heads};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c.dv == 128)
+        return launched(c.in_dtype ? launch_out_norm<128, true>(n, gate_kind, s)
+                                   : launch_out_norm<128, false>(n, gate_kind, s));
+    return launched(c.in_dtype ? launch_out_norm<64, true>(n, gate_kind, s)
+                               : launch_out_norm<64, false>(n, gate_kind, s));
+}
+
+}  // extern "C"

@@ -155,7 +155,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 
 // Wait for phase `phase` of `bar`, giving up after kWaitLimitNs.  Returns
 // false on timeout (the caller records it and returns; it never spins on).
-__device__ __noinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t phase) {
+inline __device__ __noinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t phase) {
     if (mbar_try_wait(bar, phase)) return true;
     const unsigned long long t0 = global_ns();
     for (;;) {

@@ -1,0 +1,441 @@
+// lq_linear.cuh -- linear attention with one decay per head over the FP32
+// state blobs (bits = 32), sm_100a:
+//     S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,
+// S dk x dv, row i = key channel.  Unlike the delta rule the update does not
+// read the state, so columns of S are independent and a prompt may be cut
+// along time: over tokens t0 .. t1 the state is G S + P with G the product of
+// their gates and P the state the same tokens leave from zero.
+//
+// Kernels here: one token (lin_step_kernel), a prompt token after token
+// (lin_recurrent_kernel, also the first pass of a prompt cut along time), and
+// the pass that joins the cuts (lin_scan_kernel).  The chunkwise form on the
+// tensor cores is in lq_linear_chunked.cuh.  Grouped queries and keys: value
+// head h reads query / key head h / (H / Hk).
+#pragma once
+
+#include <float.h>
+
+#include "lq_common.cuh"
+
+namespace lq {
+
+struct LinArgs {
+    uint8_t *state;
+    Layout L;
+    SlotMap map;
+    const float *S0;         // [rows, H, dk, dv] or null (zero state)
+    const void *q, *k;       // [rows, T, Hk, dk]
+    const void *v;           // [rows, T, H, dv]
+    const float *decay;      // [rows, T, H]
+    const int32_t *lengths;  // [rows] or null (all T)
+    float *out;              // [rows, T, H, dv] or null
+    int tokens;              // T
+    int work;                // rows * H
+    int group;               // value heads per query / key head
+    int qk_heads;            // Hk
+    int cont;                // 1: go on from the blob's state
+    // a prompt cut along time (nseg > 1): segment s holds tokens
+    // [s seg_len, (s + 1) seg_len)
+    int seg_len, nseg;
+    float *ws_S;   // [work, nseg, dk, dv]: a segment's own state, then the state before it
+    float *ws_g;   // [work, nseg]: product of a segment's gates
+    int *ws_bad;   // [work, nseg]: its first token with a bad gate, INT_MAX if none
+    int *ws_run;   // [work]: 0 if the blob's header refuses the call
+};
+
+constexpr int kNoBad = 0x7FFFFFFF;
+
+__device__ __forceinline__ bool lin_gate_ok(float a) { return a >= 0.f && a <= FLT_MAX; }
+
+// Row indices of token t of work item (row, hh).
+__device__ __forceinline__ size_t lin_v_row(const LinArgs &A, int row, int hh, int t) {
+    return ((size_t)row * A.tokens + t) * A.map.heads + hh;
+}
+__device__ __forceinline__ size_t lin_qk_row(const LinArgs &A, int row, int hh, int t) {
+    return ((size_t)row * A.tokens + t) * A.qk_heads + hh / A.group;
+}
+
+__device__ __forceinline__ int lin_length(const LinArgs &A, int row) {
+    return A.lengths ? min(max(__ldcg(A.lengths + row), 0), A.tokens) : A.tokens;
+}
+
+// The segment that holds a prompt's last token (0 for an empty prompt).
+__device__ __forceinline__ int lin_last_segment(const LinArgs &A, int len) {
+    return len > 0 ? (len - 1) / A.seg_len : 0;
+}
+
+// Header of a blob whose prompt has been taken in.
+__device__ __forceinline__ void lin_write_header(uint8_t *blob, int cont, bool bad) {
+    if (cont) {
+        if (bad) set_status(blob, LQ_DEV_RANGE);
+        return;
+    }
+    *reinterpret_cast<uint4 *>(blob) = make_uint4(0u, bad ? LQ_DEV_RANGE : 0u, 0u, kMagic);
+    *reinterpret_cast<float *>(blob + kHdrG) = 1.f;
+}
+
+// Whether a call that goes on from the blob may run; sets LQ_DEV_CORRUPT in a
+// header without the magic (`report`: one caller per blob).
+__device__ __forceinline__ bool lin_may_run(uint8_t *blob, bool report) {
+    const uint4 hdr = __ldcg(reinterpret_cast<const uint4 *>(blob));
+    if (report && hdr.y == 0u && hdr.w != kMagic) set_status(blob, LQ_DEV_CORRUPT);
+    return hdr.y == 0u && hdr.w == kMagic;
+}
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four consecutive inputs as floats.
+template <bool BF16>
+__device__ __forceinline__ float4 lin_load4(const uint8_t *p) {
+    if constexpr (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                           __uint_as_float(w.y & 0xFFFF0000u));
+    } else {
+        return *reinterpret_cast<const float4 *>(p);
+    }
+}
+
+// ------------------------------------------------------------- one token
+// Bound by HBM: the state is read and written once.  A CTA takes CB columns
+// of one head, all its loads in flight before the first use, a thread four
+// columns of R rows.
+template <int D, bool BF16, int CB>
+__global__ void __launch_bounds__(256, 3) lin_step_kernel(LinArgs A) {
+    constexpr int E = BF16 ? 2 : 4, NB = D / CB, CQ = CB / 4, RG = 256 / CQ, R = D / RG;
+    __shared__ float s_q[D], s_k[D];
+    __shared__ float4 s_part[RG][CQ];
+    const int tid = threadIdx.x, cq = tid % CQ, rg = tid / CQ;
+    const int w = blockIdx.x / NB, j0 = (blockIdx.x % NB) * CB + 4 * cq;
+    const int row = w / A.map.heads, hh = w - row * A.map.heads;
+
+    pdl_wait();
+    pdl_trigger();
+    const int bi = A.map.blob(w);
+    float *out = A.out + (size_t)w * D;
+    if (bi < 0) {  // no such slot (uniform over the CTA)
+        if (rg == 0) *reinterpret_cast<float4 *>(out + j0) = make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    uint8_t *blob = A.state + (size_t)bi * A.L.blob;
+    float *S = reinterpret_cast<float *>(blob + kHdrBytes) + j0;
+    float4 s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = __ldcs(reinterpret_cast<const float4 *>(S + (size_t)(rg + RG * r) * D));
+    const uint4 hdr = __ldcg(reinterpret_cast<const uint4 *>(blob));
+    const float a = A.decay[w];
+    const float4 v = lin_load4<BF16>(static_cast<const uint8_t *>(A.v) + ((size_t)w * D + j0) * E);
+    const size_t qk = ((size_t)row * A.qk_heads + hh / A.group) * D;
+    if (tid < D) s_q[tid] = load_in(A.q, qk + tid, BF16);
+    if (tid >= 256 - D) s_k[tid - (256 - D)] = load_in(A.k, qk + tid - (256 - D), BF16);
+    const bool ok = hdr.y == 0u && hdr.w == kMagic && lin_gate_ok(a);
+    __syncthreads();
+    if (!ok) {  // uniform: every CTA of this head decides the same
+        if (tid == 0 && hdr.y == 0u) set_status(blob, hdr.w == kMagic ? LQ_DEV_RANGE : LQ_DEV_CORRUPT);
+        if (rg == 0) *reinterpret_cast<float4 *>(out + j0) = make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float ki = s_k[rg + RG * r], qi = s_q[rg + RG * r];
+        s[r].x = fmaf(a, s[r].x, ki * v.x);
+        s[r].y = fmaf(a, s[r].y, ki * v.y);
+        s[r].z = fmaf(a, s[r].z, ki * v.z);
+        s[r].w = fmaf(a, s[r].w, ki * v.w);
+        __stcs(reinterpret_cast<float4 *>(S + (size_t)(rg + RG * r) * D), s[r]);
+        o.x = fmaf(s[r].x, qi, o.x);
+        o.y = fmaf(s[r].y, qi, o.y);
+        o.z = fmaf(s[r].z, qi, o.z);
+        o.w = fmaf(s[r].w, qi, o.w);
+    }
+    s_part[rg][cq] = o;
+    __syncthreads();
+    if (tid < CB) {
+        const float *p = reinterpret_cast<const float *>(s_part) + tid;
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) sum += p[g * CB];
+        out[j0 - 4 * cq + tid] = sum;
+    }
+}
+
+// ------------------------------------------- a prompt, token after token
+// 128 threads hold 16 C columns of one head's state in registers: lane % 8
+// takes the rows 4 (lane % 8) + 32 m .. + 3, lane / 8 and the warp take C
+// columns.  q, k, v and the gates arrive 16 tokens at a time through a ring
+// of three shared-memory stages; rows past the prompt arrive as zeros.  The
+// outputs of eight tokens are summed over the eight row lanes at once.
+constexpr int kLinTokens = 16;  // tokens per stage
+constexpr int kLinStages = 3;
+constexpr int kLinThreads = 128;
+
+template <int D, bool BF16, int C>
+struct LinShape {
+    static constexpr int E = BF16 ? 2 : 4;
+    static constexpr int COLS = 16 * C;               // columns of one CTA
+    static constexpr int NB = D / COLS;               // CTAs of one head (one cluster)
+    static constexpr int QB = D * E, VB = COLS * E;   // bytes of a q / k row, of a v row's columns
+    static constexpr int K_OFF = kLinTokens * QB, V_OFF = 2 * K_OFF, A_OFF = V_OFF + kLinTokens * VB;
+    static constexpr int STAGE = A_OFF + 4 * kLinTokens;
+    static constexpr uint32_t SMEM = (uint32_t)(kLinStages * STAGE);
+};
+
+template <int D, bool BF16, int C, bool PARTIAL>
+__global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
+    using SH = LinShape<D, BF16, C>;
+    constexpr int E = SH::E, M = D / 32, TB = kLinTokens;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rl = lane & 7, jt = (4 * warp + (lane >> 3)) * C;  // first column inside the CTA
+    const int w = blockIdx.x / SH::NB, jc = (blockIdx.x % SH::NB) * SH::COLS;
+    const int seg = blockIdx.y;
+    const int row = w / A.map.heads, hh = w - row * A.map.heads;
+    extern __shared__ __align__(16) uint8_t smem[];
+
+    pdl_wait();
+    pdl_trigger();
+    const int len = lin_length(A, row), last = lin_last_segment(A, len);
+    if (PARTIAL && seg >= last) return;  // not needed
+    const int bi = A.map.blob(w);
+    if (PARTIAL && bi < 0) return;
+    uint8_t *blob = A.state + (size_t)(bi < 0 ? 0 : bi) * A.L.blob;
+    bool run = bi >= 0;
+    if (!PARTIAL && A.cont) {
+        if (A.nseg > 1) {
+            run = run && A.ws_run[w] != 0;
+        } else {
+            if (run) run = lin_may_run(blob, tid == 0 && jc == 0);
+            // every CTA of the head reads the status before one may change it
+            if constexpr (SH::NB > 1)
+                asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+        }
+    }
+    const int t_begin = seg * A.seg_len, t_end = min(A.tokens, t_begin + A.seg_len);
+    if (!PARTIAL && run && seg <= last)
+        for (int s = 0; s < seg; ++s)
+            if (A.ws_bad[(size_t)w * A.nseg + s] != kNoBad) run = false;
+    const int t_stop = run ? min(len, t_end) : t_begin;
+
+    // ---- the state this segment starts from
+    float2 S[2 * M][C];
+    {
+        const float *src = nullptr;
+        if (!PARTIAL && run && seg <= last) {
+            if (A.nseg > 1) src = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D);
+            else if (A.cont) src = reinterpret_cast<const float *>(blob + kHdrBytes);
+            else if (A.S0) src = A.S0 + (size_t)w * (D * D);
+        }
+#pragma unroll
+        for (int p = 0; p < 2 * M; ++p)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int i = 4 * rl + 32 * (p >> 1) + 2 * (p & 1);
+                S[p][c] = src ? make_float2(src[(size_t)i * D + jc + jt + c], src[(size_t)(i + 1) * D + jc + jt + c])
+                              : make_float2(0.f, 0.f);
+            }
+    }
+
+    const uint8_t *qg = static_cast<const uint8_t *>(A.q), *kg = static_cast<const uint8_t *>(A.k);
+    const uint8_t *vg = static_cast<const uint8_t *>(A.v);
+    auto issue = [&](int st, int t0) {
+        uint8_t *b = smem + st * SH::STAGE;
+        constexpr int QP = SH::QB / 16, VP = SH::VB / 16;
+#pragma unroll
+        for (int x = tid; x < TB * QP; x += kLinThreads) {
+            const int r = x / QP, c = 16 * (x % QP);
+            const bool in = t0 + r < t_stop;
+            const size_t o = lin_qk_row(A, row, hh, in ? t0 + r : t_begin) * SH::QB + c;
+            if (!PARTIAL) cp_async16(b + r * SH::QB + c, qg + o, in);
+            cp_async16(b + SH::K_OFF + r * SH::QB + c, kg + o, in);
+        }
+#pragma unroll
+        for (int x = tid; x < TB * VP; x += kLinThreads) {
+            const int r = x / VP, c = 16 * (x % VP);
+            const bool in = t0 + r < t_stop;
+            cp_async16(b + SH::V_OFF + r * SH::VB + c,
+                       vg + lin_v_row(A, row, hh, in ? t0 + r : t_begin) * (size_t)(D * E) + (size_t)jc * E + c, in);
+        }
+        if (tid < TB) {
+            const bool in = t0 + tid < t_stop;
+            cp_async4(b + SH::A_OFF + 4 * tid, A.decay + lin_v_row(A, row, hh, in ? t0 + tid : t_begin), in);
+        }
+    };
+    const int n_stage = t_stop > t_begin ? (t_stop - t_begin + TB - 1) / TB : 0;
+#pragma unroll
+    for (int i = 0; i < kLinStages - 1; ++i) {
+        if (i < n_stage) issue(i, t_begin + i * TB);
+        cp_async_commit();
+    }
+
+    float gprod = 1.f;
+    int bad = kNoBad, t_done = t_stop;
+#pragma unroll 1
+    for (int i = 0; i < n_stage && bad == kNoBad; ++i) {
+        const int t0 = t_begin + i * TB;
+        cp_async_wait<kLinStages - 2>();
+        __syncthreads();
+        if (i + kLinStages - 1 < n_stage) issue((i + kLinStages - 1) % kLinStages, t0 + (kLinStages - 1) * TB);
+        cp_async_commit();
+        uint8_t *b = smem + (i % kLinStages) * SH::STAGE;
+        int n = min(TB, t_stop - t0);
+        float al = lane < n ? reinterpret_cast<const float *>(b + SH::A_OFF)[lane] : 1.f;
+        const unsigned wrong = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(al));
+        if (wrong) {  // the prompt ends before its first bad gate (uniform over the CTA)
+            n = __ffs(wrong) - 1;
+            bad = t0 + n;
+            t_done = bad;
+            if (lane >= n) al = 1.f;
+            for (int x = tid; x < (TB - n) * SH::QB / 16; x += kLinThreads)
+                *reinterpret_cast<uint4 *>(b + SH::K_OFF + n * SH::QB + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+            for (int x = tid; x < (TB - n) * SH::VB / 16; x += kLinThreads)
+                *reinterpret_cast<uint4 *>(b + SH::V_OFF + n * SH::VB + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+            __syncthreads();
+        }
+#pragma unroll 1
+        for (int g = 0; g < TB && g < n; g += 8) {
+            float p[8][C];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint8_t *qs = b + (g + u) * SH::QB + 4 * rl * E, *ks = qs + SH::K_OFF;
+                const float a = __shfl_sync(0xFFFFFFFFu, al, g + u);
+                const float2 a2 = make_float2(a, a);
+                if (PARTIAL) gprod *= a;
+                float v[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) v[c] = load_in(b + SH::V_OFF + (g + u) * SH::VB, jt + c, BF16);
+                float2 acc[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) acc[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const float4 k4 = lin_load4<BF16>(ks + 32 * m * E);
+                    float4 q4 = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!PARTIAL) q4 = lin_load4<BF16>(qs + 32 * m * E);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const float2 v2 = make_float2(v[c], v[c]);
+                        S[2 * m][c] = __ffma2_rn(a2, S[2 * m][c], __fmul2_rn(make_float2(k4.x, k4.y), v2));
+                        S[2 * m + 1][c] = __ffma2_rn(a2, S[2 * m + 1][c], __fmul2_rn(make_float2(k4.z, k4.w), v2));
+                        if (!PARTIAL) {
+                            acc[c] = __ffma2_rn(S[2 * m][c], make_float2(q4.x, q4.y), acc[c]);
+                            acc[c] = __ffma2_rn(S[2 * m + 1][c], make_float2(q4.z, q4.w), acc[c]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) p[u][c] = acc[c].x + acc[c].y;
+            }
+            if (!PARTIAL && A.out) {
+                // sum over the row lanes; lane rl keeps token g + rl
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float r4[4], r2[2];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        r4[x] = ((rl & 4) ? p[4 + x][c] : p[x][c]) +
+                                __shfl_xor_sync(0xFFFFFFFFu, (rl & 4) ? p[x][c] : p[4 + x][c], 4);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        r2[x] = ((rl & 2) ? r4[2 + x] : r4[x]) +
+                                __shfl_xor_sync(0xFFFFFFFFu, (rl & 2) ? r4[x] : r4[2 + x], 2);
+                    p[0][c] = ((rl & 1) ? r2[1] : r2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (rl & 1) ? r2[0] : r2[1], 1);
+                }
+                if (g + rl < n) {
+                    float *o = A.out + lin_v_row(A, row, hh, t0 + g + rl) * D + jc + jt;
+                    if constexpr (C == 4)
+                        *reinterpret_cast<float4 *>(o) = make_float4(p[0][0], p[0][1], p[0][2], p[0][3]);
+                    else
+#pragma unroll
+                        for (int c = 0; c < C; ++c) o[c] = p[0][c];
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+
+    if (PARTIAL) {
+        float *dst = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D) + jc + jt;
+#pragma unroll
+        for (int p = 0; p < 2 * M; ++p)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int i = 4 * rl + 32 * (p >> 1) + 2 * (p & 1);
+                dst[(size_t)i * D + c] = S[p][c].x;
+                dst[(size_t)(i + 1) * D + c] = S[p][c].y;
+            }
+        if (tid == 0 && jc == 0) {
+            A.ws_g[(size_t)w * A.nseg + seg] = gprod;
+            A.ws_bad[(size_t)w * A.nseg + seg] = bad;
+        }
+        return;
+    }
+    if (A.out)  // no outputs past the prompt's end
+        for (int x = tid; x < (t_end - t_done) * SH::COLS; x += kLinThreads)
+            A.out[lin_v_row(A, row, hh, t_done + x / SH::COLS) * D + jc + x % SH::COLS] = 0.f;
+    if (run && (bad != kNoBad || seg == last)) {  // this segment holds the prompt's end
+        float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + jc + jt;
+#pragma unroll
+        for (int p = 0; p < 2 * M; ++p)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int i = 4 * rl + 32 * (p >> 1) + 2 * (p & 1);
+                dst[(size_t)i * D + c] = S[p][c].x;
+                dst[(size_t)(i + 1) * D + c] = S[p][c].y;
+            }
+        if (tid == 0 && jc == 0) lin_write_header(blob, A.cont, bad != kNoBad);
+    }
+}
+
+// ------------------------------------- joining a prompt cut along time
+// In place: each segment's own state becomes the state before that segment.
+// One thread takes four entries of one head through all segments.
+template <int D>
+__global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs A) {
+    constexpr int NB = D * D / 1024;
+    const int w = blockIdx.x / NB, e = (blockIdx.x % NB) * 1024 + 4 * threadIdx.x;
+    const int row = w / A.map.heads;
+    pdl_wait();
+    pdl_trigger();
+    const int bi = A.map.blob(w);
+    if (bi < 0) return;
+    uint8_t *blob = A.state + (size_t)bi * A.L.blob;
+    float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (A.cont) {
+        const bool one = e == 0;
+        const bool run = lin_may_run(blob, one);
+        if (one) A.ws_run[w] = run;
+        if (!run) return;
+        carry = *reinterpret_cast<const float4 *>(blob + kHdrBytes + 4 * (size_t)e);
+    } else if (A.S0) {
+        carry = *reinterpret_cast<const float4 *>(A.S0 + (size_t)w * (D * D) + e);
+    }
+    const int last = lin_last_segment(A, lin_length(A, row));
+    float *S = A.ws_S + (size_t)w * A.nseg * (D * D) + e;
+    const float *g = A.ws_g + (size_t)w * A.nseg;
+#pragma unroll 4
+    for (int s = 0; s < last; ++s) {
+        float4 *at = reinterpret_cast<float4 *>(S + (size_t)s * (D * D));
+        const float4 own = *at;
+        const float gs = g[s];
+        *at = carry;
+        carry.x = fmaf(gs, carry.x, own.x);
+        carry.y = fmaf(gs, carry.y, own.y);
+        carry.z = fmaf(gs, carry.z, own.z);
+        carry.w = fmaf(gs, carry.w, own.w);
+    }
+    *reinterpret_cast<float4 *>(S + (size_t)last * (D * D)) = carry;
+}
+
+}  // namespace lq

@@ -1,0 +1,430 @@
+"""Linear attention with one decay per head on the GPU: one token, prompts,
+slot lists and prompts cut along time, against the recurrence in 64 bits."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+# Relative 2-norm of an output or state.  A value is a sum of terms, each
+# rounded once or twice per token it is carried (about 1 / (1 - gate) = 40 to
+# 64 tokens here) and once per key channel it is summed over (<= 128): some
+# 256 independent roundings of at most 2^-24, so 16 x 2^-24 = 2^-20; twice
+# that where an accumulator truncates.
+REL = 2.0 ** -19
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from linear_attention_recurrent_lq_b200 import build
+    build.build()
+
+
+def B():
+    from linear_attention_recurrent_lq_b200 import binding
+    return binding
+
+
+def inputs(seed, n, t, h, hk, d, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def randn(*s):
+        return torch.randn(s, generator=g, device="cuda")
+
+    q, k = randn(n, t, hk, d), randn(n, t, hk, d)
+    q, k = (x / x.norm(dim=-1, keepdim=True) for x in (q, k))
+    a = torch.exp(-torch.nn.functional.softplus(randn(n, t, h) - 4))
+    return dict(q=q.to(dtype), k=k.to(dtype), v=randn(n, t, h, d).to(dtype), decay=a, S0=randn(n, h, d, d))
+
+
+def reference(x, S0, lengths=None):
+    """Outputs and final state in 64 bits, token by token; tokens behind a
+    row's length leave its state as it is and give zeros."""
+    n, t, h, d = x["v"].shape
+    g = h // x["q"].shape[2]
+    q, k = (x[name].double().repeat_interleave(g, 2) for name in ("q", "k"))
+    v, a = x["v"].double(), x["decay"].double()
+    S = torch.zeros(n, h, d, d, dtype=torch.float64, device="cuda") if S0 is None else S0.double().clone()
+    out = torch.zeros(n, t, h, d, dtype=torch.float64, device="cuda")
+    for i in range(t):
+        new = S * a[:, i, :, None, None] + k[:, i, :, :, None] * v[:, i, :, None, :]
+        o = (q[:, i, :, :, None] * new).sum(-2)
+        live = torch.ones(n, dtype=torch.bool, device="cuda") if lengths is None else lengths > i
+        S = torch.where(live[:, None, None, None], new, S)
+        out[:, i] = torch.where(live[:, None, None], o, torch.zeros_like(o))
+    return out, S
+
+
+def near(got, want, what=""):
+    got = got.double()
+    assert torch.isfinite(got).all(), what
+    err, ref = (got - want).norm().item(), want.norm().item()
+    assert err <= REL * ref, f"{what}: relative error {err / ref if ref else err:.2e}"
+
+
+def state_of(n, h, d, dtype, slots=None):
+    b = B()
+    st = b.LQState(b.make_config(slots or n, h, d, d, bits=32, in_dtype="bf16" if dtype == torch.bfloat16 else "f32"))
+    st.buf.fill_(0xA5)
+    return st
+
+
+def run_prefill(st, x, S0=None, lengths=None, cont=False, cut=True, out=True, slots=None):
+    """The call, with outputs laid between guard rows and an unused workspace
+    full of NaN."""
+    b = B()
+    n, t, h, d = x["v"].shape
+    size = n * t * h * d
+    guard = torch.full((size + 256,), 7.0, device="cuda")
+    o = guard[128:128 + size].view(n, t, h, d) if out else None
+    need = b.lq_linear_prefill_workspace(st.cfg, n, t) if cut else 0
+    ws = torch.full((max(need, 4) // 4,), float("nan"), device="cuda").view(torch.uint8) if need else None
+    args = dict(S0=S0, lengths=lengths, out=o, qk_heads=x["q"].shape[2], cont=cont)
+    if cut:
+        args["workspace"] = ws
+    else:
+        args["workspace"] = None
+    call = dict(state=st.buf, tokens=t, q=x["q"], k=x["k"], v=x["v"], decay=x["decay"])
+    if not cut:  # a null workspace reaches the library as it is
+        real = b._linear_workspace
+        b._linear_workspace = lambda *a: (None, 0)
+    try:
+        if slots is None:
+            b.lq_linear_prefill(st.cfg, **call, **args)
+        else:
+            b.lq_linear_prefill_slots(st.cfg, slots=slots, **call, **args)
+    finally:
+        if not cut:
+            b._linear_workspace = real
+    torch.cuda.synchronize()
+    assert (guard[:128] == 7.0).all() and (guard[128 + size:] == 7.0).all()
+    return o
+
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,h,hk,d", [(1, 1, 1, 128), (3, 6, 2, 64), (2, 8, 8, 128), (37, 9, 3, 128), (100, 12, 1, 64)])
+def test_step(n, h, hk, d, dtype):
+    x = inputs(1, n, 3, h, hk, d, DT[dtype])
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, DT[dtype])
+    st.init(x["S0"])
+    out = torch.full((n, h, d), float("nan"), device="cuda")
+    for t in range(3):
+        st.linear_step(*(x[name][:, t].contiguous() for name in ("q", "k", "v", "decay")), out, qk_heads=hk)
+        near(out, want[:, t], f"token {t}")
+    near(st.dequant(), S, "state")
+    assert st.check() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_step_gates_at_their_ends_and_bad_ones(d):
+    """Gates of 0 and 1 are exact; a negative, infinite or NaN gate, a set
+    status and a wrong header skip their head alone."""
+    b = B()
+    n, h = 8, 2
+    x = inputs(2, n, 1, h, h, d, torch.bfloat16)
+    x["decay"][:, 0, 0] = torch.tensor([0.0, 1.0, -1e-30, float("nan"), float("inf"), -0.0, 0.5, 0.5])
+    st = state_of(n, h, d, torch.bfloat16)
+    st.init(x["S0"])
+    st.blobs()[6 * h].view(torch.int32)[1] = 2     # status
+    st.blobs()[7 * h].view(torch.int32)[3] = 1     # magic
+    before = st.buf.clone().view(n, h, -1)
+    out = torch.full((n, h, d), float("nan"), device="cuda")
+    st.linear_step(*(x[name][:, 0].contiguous() for name in ("q", "k", "v", "decay")), out)
+    torch.cuda.synchronize()
+    skip = [2, 3, 4, 6, 7]
+    rest = [i for i in range(n) if i not in skip]
+    after = st.buf.view(n, h, -1)
+    assert (out[skip, 0] == 0).all()
+    assert torch.equal(after[skip, 0, 128:], before[skip, 0, 128:])
+    status = after[:, 0, 4:8].contiguous().view(torch.int32).flatten().tolist()
+    assert status == [0, 0, 2, 2, 2, 0, 2, 8]
+    good = {k: (v[rest] if k != "S0" else v[rest]) for k, v in x.items()}
+    want, S = reference(good, good["S0"])
+    near(out[rest], want[:, 0])
+    near(st.dequant()[rest], S)
+    y = {k: v[skip] for k, v in x.items()}
+    y["decay"] = y["decay"].clone()
+    y["decay"][:, 0, 0] = 0
+    near(out[skip, 1], reference(y, y["S0"])[0][:, 0, 1], "the head beside a skipped one")
+    assert st.check() == b.LQ_ERR_RANGE
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_step_slots(d, dtype):
+    N, h, hk = 9, 6, 3
+    rows = [5, 0, -1, 8, 9, 2]
+    x = inputs(3, len(rows), 1, h, hk, d, DT[dtype])
+    st = state_of(N, h, d, DT[dtype])
+    S0 = inputs(4, N, 1, h, hk, d, DT[dtype])["S0"]
+    st.init(S0)
+    before = st.buf.clone().view(N, -1)
+    out = torch.full((len(rows), h, d), float("nan"), device="cuda")
+    slots = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    st.linear_step_slots(slots, *(x[name][:, 0].contiguous() for name in ("q", "k", "v", "decay")), out, qk_heads=hk)
+    live = [i for i, s in enumerate(rows) if 0 <= s < N]
+    at = [rows[i] for i in live]
+    want, S = reference({k: v[live] for k, v in x.items()}, S0[at])
+    near(out[live], want[:, 0])
+    near(st.dequant()[at], S)
+    assert (out[[2, 4]] == 0).all()
+    others = [i for i in range(N) if i not in at]
+    assert torch.equal(st.buf.view(N, -1)[others], before[others])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("t", [1, 2, 15, 16, 17, 63, 64, 65, 130, 300])
+def test_prefill_lengths_of_a_prompt(t, d, dtype):
+    n, h, hk = 2, 4, 2
+    x = inputs(5, n, t, h, hk, d, DT[dtype])
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, DT[dtype])
+    near(run_prefill(st, x, S0=x["S0"]), want, "out")
+    near(st.dequant(), S, "state")
+    assert st.check() == 0
+    near(run_prefill(st, x), reference(x, None)[0], "from zero")
+    before = st.buf.clone()
+    run_prefill(st, x, out=False)                       # without outputs: the same state
+    assert torch.equal(st.buf, before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,h,hk,d,t", [(40, 12, 4, 128, 70), (80, 12, 12, 64, 100), (300, 1, 1, 128, 65), (1, 1, 1, 64, 200),
+                                        (5, 36, 12, 128, 130)])
+def test_prefill_head_layouts(n, h, hk, d, t, dtype):
+    x = inputs(6, n, t, h, hk, d, DT[dtype])
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, DT[dtype])
+    st.init(x["S0"])
+    near(run_prefill(st, x, cont=True), want, "out")
+    near(st.dequant(), S, "state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,t", [(9, 150), (7, 1100)])
+def test_prefill_ragged_rows_with_padding_full_of_nan(n, t, d, dtype):
+    h, hk = 3, 3
+    x = inputs(7, n, t, h, hk, d, DT[dtype])
+    lengths = torch.tensor([0, 1, t, t + 5, -3, t // 2, 64, 128, t - 1][:n], dtype=torch.int32, device="cuda")
+    pad = torch.arange(t, device="cuda") >= lengths[:, None].clamp(0, t)
+    want, S = reference(x, x["S0"], lengths)
+    for name in ("q", "k", "v", "decay"):
+        x[name] = x[name].masked_fill(pad.view(n, t, *[1] * (x[name].dim() - 2)), float("nan"))
+    st = state_of(n, h, d, DT[dtype])
+    out = run_prefill(st, x, S0=x["S0"], lengths=lengths)
+    near(out, want, "out")
+    assert (out[pad] == 0).all()
+    near(st.dequant(), S, "state")
+    assert st.check() == 0
+    st.init(x["S0"])
+    near(run_prefill(st, x, lengths=lengths, cont=True), want, "continued")
+    near(st.dequant(), S, "continued state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_strong_and_resetting_gates(d, dtype):
+    """Gates of 0, products far below the smallest float, and runs of 1."""
+    n, t, h = 2, 200, 4
+    x = inputs(8, n, t, h, h, d, DT[dtype])
+    a = x["decay"]
+    a[0, ::37, 0] = 0
+    a[0, 63:66, 1] = 0
+    a[0, :, 2] = 1e-3
+    a[0, :, 3] = 1
+    a[1, :, 0] = 1e-30
+    a[1, ::2, 1] = 1e-20
+    a[1, 64:128, 2] = 0
+    a[1, :, 3] = 0
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, DT[dtype])
+    out = run_prefill(st, x, S0=x["S0"])
+    for i in range(n):
+        for j in range(h):
+            near(out[i, :, j], want[i, :, j], f"out {i} {j}")
+            near(st.dequant()[i, j], S[i, j], f"state {i} {j}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("t", [100, 1500])
+@pytest.mark.parametrize("cont", [False, True])
+def test_prefill_ends_before_a_bad_gate(t, cont, d, dtype):
+    b = B()
+    n, h = 6, 2
+    x = inputs(9, n, t, h, h, d, DT[dtype])
+    ends = [0, 1, 17, t // 2, t - 1, t]
+    lengths = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    bad = [-1.0, float("nan"), float("inf"), -1e-38, float("-inf")]
+    y = dict(x, decay=x["decay"].clone())
+    for i, e in enumerate(ends[:5]):
+        y["decay"][i, e, 0] = bad[i]
+    st = state_of(n, h, d, DT[dtype])
+    if cont:
+        st.init(x["S0"])
+    out = run_prefill(st, y, S0=None if cont else x["S0"], cont=cont)
+    cut = {k: v[:, :, :1].contiguous() if k != "S0" else v[:, :1] for k, v in x.items()}
+    want, S = reference(cut, cut["S0"], lengths)
+    near(out[:, :, :1], want, "out before the gate")
+    for i, e in enumerate(ends):
+        assert (out[i, e:, 0] == 0).all()
+    near(st.dequant()[:, :1], S, "state before the gate")
+    side = {k: v[:, :, 1:].contiguous() if k != "S0" else v[:, 1:] for k, v in x.items()}
+    near(out[:, :, 1:], reference(side, side["S0"])[0], "the head beside it")
+    status = st.blobs()[:, 4:8].contiguous().view(torch.int32).view(n, h).tolist()
+    assert status == [[2, 0]] * 5 + [[0, 0]]
+    # a set status: the next call that goes on from the blobs skips these heads
+    before = st.buf.clone().view(n, h, -1)
+    out = run_prefill(st, x, cont=True)
+    assert (out[:5, :, 0] == 0).all()
+    assert torch.equal(st.buf.view(n, h, -1)[:5, 0], before[:5, 0])
+    assert st.check() == b.LQ_ERR_RANGE
+    # a wrong header is refused too
+    st.blobs()[5 * h].view(torch.int32)[3] = 0
+    out = run_prefill(st, x, cont=True)
+    assert (out[5, :, 0] == 0).all()
+    assert st.blobs()[5 * h, 4:8].view(torch.int32).item() == 8
+    # and a call from a given state writes the headers anew
+    run_prefill(st, x, S0=x["S0"])
+    assert st.check() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,h,d,t", [(1, 3, 128, 1031), (2, 2, 64, 2048), (1, 1, 128, 3001)])
+def test_prefill_cut_along_time(n, h, d, t, dtype):
+    """Few heads and a long prompt: with and without the cut."""
+    b = B()
+    x = inputs(10, n, t, h, h, d, DT[dtype])
+    x["decay"][:, 700, :] = 0
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, DT[dtype])
+    assert b.lq_linear_prefill_workspace(st.cfg, n, t) > 0
+    for cut in (True, False):
+        near(run_prefill(st, x, S0=x["S0"], cut=cut), want, f"out, cut {cut}")
+        near(st.dequant(), S, f"state, cut {cut}")
+        st.init(x["S0"])
+        near(run_prefill(st, x, cont=True, cut=cut), want, f"continued, cut {cut}")
+        near(st.dequant(), S, f"continued state, cut {cut}")
+    o = torch.empty_like(x["v"], dtype=torch.float32)
+    st.linear_prefill(t, x["q"], x["k"], x["v"], x["decay"], S0=x["S0"], out=o)   # the binding's own workspace
+    near(o, want, "own workspace")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [40, 1200])
+def test_prefill_slots(t, dtype):
+    N, h, hk, d = 6, 4, 2, 128
+    rows = [4, -1, 0, 6]
+    x = inputs(11, len(rows), t, h, hk, d, DT[dtype])
+    S0 = inputs(12, N, 1, h, hk, d, DT[dtype])["S0"]
+    st = state_of(N, h, d, DT[dtype])
+    slots = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([t, t, t - 9, t], dtype=torch.int32, device="cuda")
+    live, at = [0, 2], [4, 0]
+    others = [i for i in range(N) if i not in at]
+    for cont in (False, True):
+        st.init(S0)
+        before = st.buf.clone().view(N, -1)
+        out = run_prefill(st, x, lengths=lengths, cont=cont, slots=slots)
+        want, S = reference({k: v[live] for k, v in x.items()}, S0[at] if cont else None, lengths[live])
+        near(out[live], want)
+        assert (out[[1, 3]] == 0).all()
+        near(st.dequant()[at], S)
+        assert torch.equal(st.buf.view(N, -1)[others], before[others])
+
+
+@pytest.mark.parametrize("t", [0, 5])
+def test_prefill_of_no_tokens(t):
+    n, h, d = 2, 3, 64
+    x = inputs(13, n, t, h, h, d, torch.bfloat16)
+    st = state_of(n, h, d, torch.bfloat16)
+    zero = torch.zeros(n, dtype=torch.int32, device="cuda")
+    run_prefill(st, x, S0=x["S0"], lengths=zero)
+    assert torch.equal(st.dequant(), x["S0"]) and st.check() == 0
+    run_prefill(st, x, lengths=zero, cont=True)
+    assert torch.equal(st.dequant(), x["S0"])
+    run_prefill(st, x, lengths=zero)
+    assert (st.dequant() == 0).all() and st.check() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_then_tokens_equals_one_prompt(d):
+    n, h, hk, t = 3, 6, 2, 90
+    x = inputs(14, n, t, h, hk, d, torch.bfloat16)
+    want, S = reference(x, None)
+    st = state_of(n, h, d, torch.bfloat16)
+    head = {k: v[:, :77].contiguous() if k != "S0" else v for k, v in x.items()}
+    near(run_prefill(st, head), want[:, :77])
+    mid = {k: v[:, 77:85].contiguous() if k != "S0" else v for k, v in x.items()}
+    near(run_prefill(st, mid, cont=True), want[:, 77:85])
+    out = torch.empty(n, h, d, device="cuda")
+    for i in range(85, t):
+        st.linear_step(*(x[name][:, i].contiguous() for name in ("q", "k", "v", "decay")), out, qk_heads=hk)
+        near(out, want[:, i])
+    near(st.dequant(), S)
+
+
+def test_captured_calls_replay_on_another_stream():
+    """A prompt cut along time and a token step in one graph, replayed twice;
+    two such graphs of different states run side by side."""
+    n, h, d, t = 1, 2, 128, 1500
+    graphs, states, outs, wants = [], [], [], []
+    for i in range(2):
+        x = inputs(20 + i, n, t, h, h, d, torch.bfloat16)
+        y = inputs(30 + i, n, 1, h, h, d, torch.bfloat16)
+        st = state_of(n, h, d, torch.bfloat16)
+        o, o1 = torch.empty(n, t, h, d, device="cuda"), torch.empty(n, h, d, device="cuda")
+
+        def calls():
+            st.linear_prefill(t, x["q"], x["k"], x["v"], x["decay"], S0=x["S0"], out=o)
+            st.linear_step(y["q"][:, 0].contiguous(), y["k"][:, 0].contiguous(), y["v"][:, 0].contiguous(),
+                           y["decay"][:, 0].contiguous(), o1)
+
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            calls()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            calls()
+        both = {k: (torch.cat([x[k], y[k]], 1) if k != "S0" else x[k]) for k in x}
+        wants.append(reference(both, x["S0"]))
+        graphs.append(g); states.append((st, x, y)); outs.append((o, o1))
+    for _ in range(2):
+        for o, o1 in outs:
+            o.fill_(float("nan")); o1.fill_(float("nan"))
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, o1), (st, _, _), (want, S) in zip(outs, states, wants):
+            near(o, want[:, :t])
+            near(o1, want[:, t])
+            near(st.dequant(), S)
+
+
+def test_call_on_a_given_stream():
+    n, h, d, t = 1, 2, 128, 1500
+    x = inputs(40, n, t, h, h, d, torch.bfloat16)
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, torch.bfloat16)
+    out = torch.empty(n, t, h, d, device="cuda")
+    torch.cuda.synchronize()
+    for s in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream, 0):
+        out.zero_()
+        torch.cuda.synchronize()
+        st.linear_prefill(t, x["q"], x["k"], x["v"], x["decay"], S0=x["S0"], out=out, stream=s)
+        torch.cuda.synchronize()
+        near(out, want)
+        near(st.dequant(), S)
