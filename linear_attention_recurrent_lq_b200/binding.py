@@ -145,9 +145,15 @@ def _ptr(x) -> int | None:
 # that is current, where the library launches).  Raw integer addresses are
 # passed through unchecked: their owner vouches for them.
 
-def _dt(name):
-    import torch
-    return {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32, "u8": torch.uint8}[name]
+_DTYPES = {}
+
+
+def _dtypes():
+    """Element types by their short names (filled at the first call)."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update(f32=torch.float32, bf16=torch.bfloat16, i32=torch.int32, u8=torch.uint8)
+    return _DTYPES
 
 
 def _in_dt(cfg) -> str:
@@ -155,35 +161,54 @@ def _in_dt(cfg) -> str:
 
 
 def _validate(*specs):
-    """Check (tensor, what, dtype(s), numel, at_least) specs: first every
-    element type and count, then that every tensor sits on the current CUDA
-    device.  ValueError on the first mismatch; None and integer addresses
-    pass."""
-    import torch
-    ts = [sp for sp in specs if sp[0] is not None and not isinstance(sp[0], int)]
-    for x, what, dtype, numel, at_least in ts:
-        want = dtype if isinstance(dtype, tuple) else (dtype,)
-        if x.dtype not in tuple(_dt(d) for d in want):
-            raise ValueError(f"{what}: dtype {x.dtype}, expected {' or '.join(want)}")
+    """Check (tensor, what, dtype, numel, at_least) specs: first every element
+    type and count, then that every tensor sits on the current CUDA device.
+    ValueError on the first mismatch; None and integer addresses pass.  Runs
+    before every call, where a token's kernel may take 3 us: one attribute of
+    a tensor read per check."""
+    dtypes = _dtypes()
+    ts = []
+    for sp in specs:
+        x, what, dtype, numel, at_least = sp
+        if x is None or isinstance(x, int):
+            continue
+        if x.dtype is not dtypes[dtype]:
+            raise ValueError(f"{what}: dtype {x.dtype}, expected {dtype}")
         if numel is not None:
             n = x.numel()
             if (n < numel) if at_least else (n != numel):
                 raise ValueError(f"{what}: {n} elements, expected {'at least ' if at_least else ''}{numel}")
+        ts.append(sp)
+    dev = None
     for x, what, *_ in ts:
-        if x.device.type != "cuda":
+        if not x.is_cuda:
             raise ValueError(f"{what}: on {x.device}, expected a CUDA tensor")
-        dev = torch.cuda.current_device()
-        if x.device.index != dev:
-            raise ValueError(f"{what}: on cuda:{x.device.index}, but the library launches on cuda:{dev}")
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device()
+        if x.get_device() != dev:
+            raise ValueError(f"{what}: on cuda:{x.get_device()}, but the library launches on cuda:{dev}")
 
 
 def _spec(x, what, dtype, numel=None, at_least=False):
     return (x, what, dtype, numel, at_least)
 
 
+_BLOB_BYTES = {}
+
+
+def _blob_bytes(cfg) -> int:
+    """lq_state_bytes by the configuration's bytes (0: not built)."""
+    key = bytes(cfg)
+    n = _BLOB_BYTES.get(key)
+    if n is None:
+        n = _BLOB_BYTES[key] = lib.lq_state_bytes(ctypes.byref(cfg))
+    return n
+
+
 def _state_spec(cfg, state, num_slots=None, what="state"):
     n = cfg.num_slots if num_slots is None else num_slots
-    bb = lib.lq_state_bytes(ctypes.byref(cfg))
+    bb = _blob_bytes(cfg)
     return _spec(state, what, "u8", n * cfg.num_heads * bb if bb else None, at_least=True)
 
 
@@ -201,12 +226,18 @@ def _dense_spec(cfg, x, what, rows):
 
 
 
+_HAS_CUDA = None
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        global _HAS_CUDA
         import torch
-        if not torch.cuda.is_available():
+        if _HAS_CUDA is None:
+            _HAS_CUDA = torch.cuda.is_available()
+        if not _HAS_CUDA:
             return None
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

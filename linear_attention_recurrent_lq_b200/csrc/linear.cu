@@ -7,6 +7,7 @@
 #include "lq_common.cuh"
 #include "lq_host.cuh"
 #include "lq_linear.cuh"
+#include "lq_linear_chunked.cuh"
 #include "lq_norms.cuh"
 
 using namespace lq;
@@ -118,8 +119,28 @@ lq_status launch_recurrent(const LinArgs &a, cudaStream_t s) {
                                    SH::SMEM, s, a));
 }
 
+template <int D>
+lq_status launch_chunked(const LinArgs &a, cudaStream_t s) {
+    const uint32_t smem = LcShape<D>::SMEM;
+    if (a.nseg > 1) {
+        auto k = lin_chunk_kernel<D, true>;
+        if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;
+        if (launch_cluster(k, dim3((unsigned)a.work, (unsigned)(a.nseg - 1)), kLcThreads, 1, smem, s, a) != cudaSuccess)
+            return LQ_ERR_CUDA;
+        if (launch_pdl(lin_scan_kernel<D>, a.work * (D * D / 1024), 256, 0u, s, a) != cudaSuccess) return LQ_ERR_CUDA;
+    }
+    auto k = lin_chunk_kernel<D, false>;
+    if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;
+    return launched(launch_cluster(k, dim3((unsigned)a.work, (unsigned)a.nseg), kLcThreads, 1, smem, s, a));
+}
+
+// bf16 prompts from here on take the chunkwise form
+constexpr int kMinChunked = 32;
+
 template <int D, bool BF16>
 lq_status launch_prefill(const LinArgs &a, cudaStream_t s) {
+    if constexpr (BF16)
+        if (a.tokens >= kMinChunked) return launch_chunked<D>(a, s);
     // few heads: 16 columns per CTA, else 64
     if ((int64_t)a.work * a.nseg * (D / 64) < 2 * kSms) return launch_recurrent<D, BF16, 1>(a, s);
     return launch_recurrent<D, BF16, 4>(a, s);
