@@ -8,6 +8,7 @@
 #include "lq_host.cuh"
 #include "lq_linear.cuh"
 #include "lq_linear_chunked.cuh"
+#include "lq_linear_pipe.cuh"
 #include "lq_norms.cuh"
 
 using namespace lq;
@@ -119,19 +120,48 @@ lq_status launch_recurrent(const LinArgs &a, cudaStream_t s) {
                                    SH::SMEM, s, a));
 }
 
+// A [rows, cols] bf16 tensor as boxes of 64 rows x 64 columns, 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+    const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 lq_status launch_chunked(const LinArgs &a, cudaStream_t s) {
-    const uint32_t smem = LcShape<D>::SMEM;
     if (a.nseg > 1) {
+        const uint32_t smem = LcShape<D>::SMEM;
         auto k = lin_chunk_kernel<D, true>;
         if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;
         if (launch_cluster(k, dim3((unsigned)a.work, (unsigned)(a.nseg - 1)), kLcThreads, 1, smem, s, a) != cudaSuccess)
             return LQ_ERR_CUDA;
         if (launch_pdl(lin_scan_kernel<D>, a.work * (D * D / 1024), 256, 0u, s, a) != cudaSuccess) return LQ_ERR_CUDA;
     }
-    auto k = lin_chunk_kernel<D, false>;
+    CUtensorMap mq, mk, mv;
+    const uint64_t rows = (uint64_t)(a.work / a.map.heads) * a.tokens;
+    if (!make_map(&mq, a.q, (uint64_t)a.qk_heads * D, rows) || !make_map(&mk, a.k, (uint64_t)a.qk_heads * D, rows) ||
+        !make_map(&mv, a.v, (uint64_t)a.map.heads * D, rows))
+        return LQ_ERR_CUDA;
+    const uint32_t smem = LpShape<D>::SMEM;
+    auto k = lin_pipe_kernel<D>;
     if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;
-    return launched(launch_cluster(k, dim3((unsigned)a.work, (unsigned)a.nseg), kLcThreads, 1, smem, s, a));
+    const int grid = persistent_grid(k, kLpThreads, smem, a.work * a.nseg);
+    if (grid <= 0) return LQ_ERR_CUDA;
+    return launched(launch_pdl(k, grid, kLpThreads, smem, s, a, mq, mk, mv));
 }
 
 // bf16 prompts from here on take the chunkwise form

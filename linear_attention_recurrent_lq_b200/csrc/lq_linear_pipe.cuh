@@ -1,0 +1,584 @@
+// lq_linear_pipe.cuh -- a prompt of linear attention in the chunkwise form on
+// the tensor cores, the chunks of all heads in one pipeline per SM (bf16 q,
+// k, v; sm_100a: TMA, tcgen05, tensor memory).
+//
+// A chunk is up to 64 tokens.  The first token's gate is applied to the
+// incoming state (S = a_0 S_before); with G_t the product of the gates behind
+// it up to t (G_0 = 1),
+//     o_t = G_t ( S^T q_t + sum_{s <= t} (q_t . k_s / G_s) v_s ),
+//     S'  = G_last ( S + sum_s (k_s / G_s) v_s^T ),
+// so nothing has to be scaled between the two products of o_t.  A chunk ends
+// before a token that would take G below 2^-64: 1 / G stays far inside FP32,
+// and a gate of 0 starts a chunk, where it clears the state exactly.
+//
+// Precision: q, k and v are bf16 as they come; every FP32 operand (the state,
+// the scores, k / G) is cut into three bf16 pieces that hold its 24 bits
+// exactly, multiplied smallest first, and summed in FP32.
+//
+// One CTA per SM walks the work items (a head, or a segment of a prompt cut
+// along time) b, b + grid, ... as one stream of chunks.  Its warps:
+//   0 .. 7   the state, in registers (lane = value channel, the two groups of
+//            four warps take half of the key channels each): its three pieces
+//            to tensor memory as an A operand, the outputs from tensor memory
+//            to global memory, the update
+//   8, 9     the scores: from tensor memory, times 1 / G, masked, three pieces
+//            to shared memory
+//   10, 11   k / G in three pieces to shared memory
+//   12       one thread issues every product, in the order Q K^T of chunk c,
+//            V^T P^T of c - 1, V^T K' of c, S^T Q^T of c
+//   13       the feeder: gates and their products, the chunk's bounds, and the
+//            TMA loads, up to three chunks ahead
+// They meet in mbarriers only.  Bound by HBM at 1284 bytes per token and head
+// (d = 128): 3440 clocks per chunk and SM, next to about 2500 of tensor time
+// and 2300 issue slots per scheduler.
+#pragma once
+
+#include <cuda.h>
+
+#include "lq_linear_chunked.cuh"
+
+namespace lq {
+
+constexpr int kLpThreads = 14 * 32;
+constexpr int kLpStages = 3;   // chunks of q, k, v in shared memory
+constexpr int kLpRing = 4;     // chunk descriptions
+constexpr float kLpMinGate = 0x1p-64f;
+// tensor memory: Q K^T | O^T, two | S pieces | V^T K'
+constexpr uint32_t kLpQK = 0, kLpO = 64, kLpSp = 192, kLpD = 384;
+
+enum : int { kLpFirst = 1, kLpLast = 2, kLpFinal = 4, kLpBad = 8, kLpNone = 16, kLpEnd = 32 };
+
+struct __align__(16) LpSlot {
+    float G[64], inv[64];  // products of gates, and one over them (0 behind the chunk)
+    int w, t0, n, flags;
+    int zero_end, seg;     // outputs from t0 + n up to here are zeros (last chunk of an item)
+    float a_first, g_next; // gate of the item's first token; G_last times the next chunk's first gate
+};
+
+template <int D>
+struct LpShape {
+    static constexpr int KB = D / 64;
+    // a stage: KB blocks of 128 rows (64 of Q, 64 of K) x 128 bytes, KB blocks of 64 rows of V
+    static constexpr uint32_t V = KB * 16384u, STAGE = KB * 24576u;
+    static constexpr uint32_t P = kLpStages * STAGE, K = P + 3u * 8192u, RING = K + 3u * KB * 8192u;
+    static constexpr uint32_t BAR = RING + kLpRing * (uint32_t)sizeof(LpSlot);
+    static constexpr uint32_t SMEM = BAR + 256u + 1024u;
+    static constexpr int SW = D / 16;  // warps that hold state: all eight, or the four whose lanes are < 64
+};
+
+struct LpBars {
+    uint64_t full[kLpStages], empty[kLpStages], ring_full[kLpRing], ring_free[kLpRing];
+    uint64_t qk_done, qk_free, p_ready, k_ready, s_ready, y_done, d_done, d_free, o_done[2], o_free[2];
+    uint32_t tmem, fail;
+};
+static_assert(sizeof(LpBars) <= 256, "barrier space");
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 16 columns, without the wait (tmem_ld_wait before the first use)
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Wait for the loads above; the registers pass through, so that no use is
+// scheduled before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 ::"memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kLpThreads, 1)
+    lin_pipe_kernel(const LinArgs A, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv) {
+    using SH = LpShape<D>;
+    constexpr int KB = SH::KB, HD = D / 2, C = 64;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    LpSlot *ring = reinterpret_cast<LpSlot *>(smem + SH::RING);
+    LpBars *bars = reinterpret_cast<LpBars *>(smem + SH::BAR);
+    const uint32_t base = smem_u32(smem);
+
+    if (tid == 0) {
+        for (int i = 0; i < kLpStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 1);
+        }
+        for (int i = 0; i < kLpRing; ++i) {
+            mbar_init(&bars->ring_full[i], 1);
+            mbar_init(&bars->ring_free[i], SH::SW + 5);  // state, score and key warps, the issuer
+        }
+        mbar_init(&bars->qk_done, 1);
+        mbar_init(&bars->qk_free, 2);
+        mbar_init(&bars->p_ready, 2);
+        mbar_init(&bars->k_ready, 2);
+        mbar_init(&bars->s_ready, SH::SW);
+        mbar_init(&bars->y_done, 1);
+        mbar_init(&bars->d_done, 1);
+        mbar_init(&bars->d_free, SH::SW);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->o_done[i], 1);
+            mbar_init(&bars->o_free[i], SH::SW);
+        }
+        bars->fail = 0u;
+        fence_mbar_init();
+    }
+    pdl_wait();
+    if (warp == 12) tmem_alloc(&bars->tmem, 512u);  // after the wait: a kernel still running may need it
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int items = A.work * A.nseg;
+
+    bool ok = true;  // false: a wait gave up; every role then leaves
+    auto wait = [&](uint64_t *b, uint32_t phase) {
+        if (!mbar_wait_bounded(b, phase & 1u)) ok = false;
+    };
+    auto arrive = [&](uint64_t *b) {  // one arrival per warp, after all its lanes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+    };
+    auto tile_off = [&](int r, int c, uint32_t block) -> uint32_t {  // row r, 16-byte piece c
+        return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+    };
+
+    if (warp == 13) {
+        // ------------------------------------------------------- the feeder
+        uint32_t r = 0, c = 0;
+        auto slot_wait = [&]() -> LpSlot * {
+            if (r >= kLpRing) wait(&bars->ring_free[r % kLpRing], r / kLpRing - 1u);
+            return ring + r % kLpRing;
+        };
+#pragma unroll 1
+        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+            const int w = it / A.nseg, seg = it - w * A.nseg;
+            const int row = w / A.map.heads, hh = w - row * A.map.heads;
+            const int len = lin_length(A, row), last = lin_last_segment(A, len);
+            const int bi = A.map.blob(w);
+            uint8_t *blob = A.state + (size_t)(bi < 0 ? 0 : bi) * A.L.blob;
+            bool run = bi >= 0;
+            if (A.cont && run) run = A.nseg > 1 ? A.ws_run[w] != 0 : lin_may_run(blob, lane == 0);
+            if (run && seg <= last) {
+                bool before = false;
+                for (int s = lane; s < seg; s += 32) before |= A.ws_bad[(size_t)w * A.nseg + s] != kNoBad;
+                if (__any_sync(0xFFFFFFFFu, before)) run = false;
+            }
+            const int t_begin = seg * A.seg_len, t_end = min(A.tokens, t_begin + A.seg_len);
+            const int t_stop = run ? min(len, t_end) : t_begin;
+            const bool holds_end = run && seg == last;
+            const float *gates = A.decay + lin_v_row(A, row, hh, 0);
+            const size_t gs = (size_t)A.map.heads;
+            auto gate = [&](int t) -> float { return t < t_stop ? __ldcg(gates + (size_t)t * gs) : 1.f; };
+            float a0 = gate(t_begin + 2 * lane), a1 = gate(t_begin + 2 * lane + 1), a64 = gate(t_begin + C);
+            const float first = __shfl_sync(0xFFFFFFFFu, a0, 0);
+            const bool first_bad = t_begin < t_stop && !lin_gate_ok(first);
+            if (t_begin >= t_stop || first_bad) {  // no chunk
+                LpSlot *sl = slot_wait();
+                if (lane == 0) {
+                    sl->w = w; sl->seg = seg; sl->t0 = t_begin; sl->n = 0; sl->zero_end = t_end;
+                    sl->flags = kLpNone | kLpFirst | kLpLast | (holds_end || first_bad ? kLpFinal : 0) |
+                                (first_bad ? kLpBad : 0);
+                }
+                arrive(&bars->ring_full[r % kLpRing]);
+                ++r;
+                continue;
+            }
+            const int xq = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens;
+#pragma unroll 1
+            for (int t0 = t_begin; t0 < t_stop && ok;) {
+                // the gates of the next chunk, if this one has all 64 tokens
+                const float n0 = gate(t0 + C + 2 * lane), n1 = gate(t0 + C + 2 * lane + 1), n64 = gate(t0 + 2 * C);
+                const unsigned w0 = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(a0));
+                const unsigned w1 = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(a1));
+                const int nb = min(w0 ? 2 * (__ffs(w0) - 1) : C, w1 ? 2 * (__ffs(w1) - 1) + 1 : C);
+                float p = (lane ? a0 : 1.f) * a1, pre = p;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const float x = __shfl_up_sync(0xFFFFFFFFu, pre, d);
+                    if (lane >= d) pre *= x;
+                }
+                const float before = __shfl_up_sync(0xFFFFFFFFu, pre, 1);
+                const float g0 = lane ? before * a0 : 1.f, g1 = pre;  // up to tokens 2 lane, 2 lane + 1
+                const unsigned l0 = __ballot_sync(0xFFFFFFFFu, !(g0 >= kLpMinGate));
+                const unsigned l1 = __ballot_sync(0xFFFFFFFFu, !(g1 >= kLpMinGate));
+                const int nl = min(l0 ? 2 * (__ffs(l0) - 1) : C, l1 ? 2 * (__ffs(l1) - 1) + 1 : C);
+                const int rem = t_stop - t0, n = min(min(C, rem), min(nb, nl));
+                const float ev = __shfl_sync(0xFFFFFFFFu, a0, (n >> 1) & 31), od = __shfl_sync(0xFFFFFFFFu, a1, (n >> 1) & 31);
+                const float next = n == C ? a64 : (n & 1) ? od : ev;
+                const bool bad = n < rem && !lin_gate_ok(next), end = n == rem || bad;
+                const float ge = __shfl_sync(0xFFFFFFFFu, g0, ((n - 1) >> 1) & 31), go = __shfl_sync(0xFFFFFFFFu, g1, ((n - 1) >> 1) & 31);
+                const float g_last = ((n - 1) & 1) ? go : ge;
+
+                const uint32_t st = c % kLpStages;
+                if (c >= kLpStages) wait(&bars->empty[st], c / kLpStages - 1u);
+                if (lane == 0 && ok) {
+                    uint8_t *sp = smem + st * SH::STAGE;
+                    mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        tma_load_2d(sp + kb * 16384, &mq, xq + 64 * kb, y0 + t0, &bars->full[st]);
+                        tma_load_2d(sp + kb * 16384 + 8192, &mk, xq + 64 * kb, y0 + t0, &bars->full[st]);
+                        tma_load_2d(sp + SH::V + kb * 8192, &mv, xv + 64 * kb, y0 + t0, &bars->full[st]);
+                    }
+                }
+                LpSlot *sl = slot_wait();
+                *reinterpret_cast<float2 *>(sl->G + 2 * lane) = make_float2(g0, g1);
+                *reinterpret_cast<float2 *>(sl->inv + 2 * lane) =
+                    make_float2(2 * lane < n ? __fdiv_rn(1.f, g0) : 0.f, 2 * lane + 1 < n ? __fdiv_rn(1.f, g1) : 0.f);
+                if (lane == 0) {
+                    sl->w = w; sl->seg = seg; sl->t0 = t0; sl->n = n; sl->zero_end = t_end;
+                    sl->a_first = first;
+                    sl->g_next = end ? g_last : g_last * next;
+                    sl->flags = (t0 == t_begin ? kLpFirst : 0) | (end ? kLpLast : 0) |
+                                (end && (holds_end || bad) ? kLpFinal : 0) | (bad ? kLpBad : 0);
+                }
+                arrive(&bars->ring_full[r % kLpRing]);
+                ++r;
+                ++c;
+                t0 += n;
+                if (end) break;
+                if (n == C) {
+                    a0 = n0; a1 = n1; a64 = n64;
+                } else {
+                    a0 = gate(t0 + 2 * lane); a1 = gate(t0 + 2 * lane + 1); a64 = gate(t0 + C);
+                }
+            }
+        }
+        LpSlot *sl = slot_wait();
+        if (lane == 0) sl->flags = kLpEnd;
+        arrive(&bars->ring_full[r % kLpRing]);
+        // what has been asked for lands before the CTA leaves
+        for (uint32_t i = c > kLpStages ? c - kLpStages : 0u; i < c; ++i)
+            mbar_wait_bounded(&bars->full[i % kLpStages], (i / kLpStages) & 1u);
+    } else if (warp == 12) {
+        // ------------------------------------------------------- the issuer
+        constexpr uint32_t id64 = lc_idesc(128, 64, 0, 0), idpv = lc_idesc(128, 64, 1, 0), idpv2 = lc_idesc(128, 32, 1, 0),
+                           idd = lc_idesc(128, D, 1, 1);
+        constexpr uint32_t vlbo = KB > 1 ? 8192u : 0u;  // D = 64: lanes 64 .. repeat the others
+        uint32_t c = 0;
+        auto pv = [&](uint32_t i) {  // O^T += V^T P^T of chunk i
+            wait(&bars->p_ready, i);
+            if (lane == 0 && ok) {
+                tc_fence_after();
+                const uint32_t vb = base + (i % kLpStages) * SH::STAGE + SH::V, o = tmem + kLpO + 64u * (i & 1u);
+#pragma unroll
+                for (int x = 2; x >= 0; --x) {
+                    const uint32_t pb = base + SH::P + (uint32_t)x * 8192u;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)  // tokens 32 .. reach rows 32 .. only
+                        if (ks < 2)
+                            lc_mma_ss(o, lc_desc(vb + ks * 2048u, vlbo), lc_desc(pb + ks * 32u, 16u), idpv, 1u);
+                        else
+                            lc_mma_ss(o + 32u, lc_desc(vb + ks * 2048u, vlbo), lc_desc(pb + 4096u + ks * 32u, 16u), idpv2, 1u);
+                }
+                umma_commit(&bars->o_done[i & 1u]);
+                umma_commit(&bars->empty[i % kLpStages]);
+            }
+            __syncwarp();
+        };
+#pragma unroll 1
+        for (uint32_t r = 0; ok; ++r) {
+            wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            const int flags = ok ? ring[r % kLpRing].flags : kLpEnd;
+            arrive(&bars->ring_free[r % kLpRing]);
+            if (flags & kLpEnd) break;
+            if (flags & kLpNone) continue;
+            const uint32_t sb = base + (c % kLpStages) * SH::STAGE;
+            wait(&bars->full[c % kLpStages], c / kLpStages);
+            if (c > 0) wait(&bars->qk_free, c - 1u);
+            if (lane == 0 && ok) {  // Q K^T; rows 64 .. 127 (K K^T) are not used
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t o = sb + (uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u;
+                    lc_mma_ss(tmem + kLpQK, lc_desc(o, 16u), lc_desc(o + 8192u, 16u), id64, ks > 0);
+                }
+                umma_commit(&bars->qk_done);
+            }
+            __syncwarp();
+            if (c > 0) pv(c - 1u);
+            wait(&bars->k_ready, c);
+            if (c > 0) wait(&bars->d_free, c - 1u);
+            if (lane == 0 && ok) {  // V^T K'
+                tc_fence_after();
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks)
+                        lc_mma_ss(tmem + kLpD, lc_desc(sb + SH::V + ks * 2048u, vlbo),
+                                  lc_desc(base + SH::K + (uint32_t)x * (KB * 8192u) + ks * 2048u, 8192u), idd, x < 2 || ks > 0);
+                umma_commit(&bars->d_done);
+            }
+            __syncwarp();
+            wait(&bars->s_ready, c);
+            if (c > 1) wait(&bars->o_free[c & 1u], c / 2u - 1u);
+            if (lane == 0 && ok) {  // S^T Q^T
+                tc_fence_after();
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        lc_mma_ts(tmem + kLpO + 64u * (c & 1u), tmem + kLpSp + (uint32_t)(x * HD + 8 * ks),
+                                  lc_desc(sb + (uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u, 16u), id64,
+                                  x < 2 || ks > 0);
+                umma_commit(&bars->y_done);
+            }
+            __syncwarp();
+            ++c;
+        }
+        if (c > 0 && ok) pv(c - 1u);
+        // every product has ended before tensor memory is given back
+        if (c > 0) mbar_wait_bounded(&bars->o_done[(c - 1u) & 1u], ((c - 1u) / 2u) & 1u);
+    } else if (warp >= 10) {
+        // ------------------------------------------------- k / G, in pieces
+        constexpr int NP = 8 * KB;
+        uint32_t c = 0;
+#pragma unroll 1
+        for (uint32_t r = 0; ok; ++r) {
+            wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            const LpSlot *sl = ring + r % kLpRing;
+            const int flags = ok ? sl->flags : kLpEnd;
+            if (flags & (kLpEnd | kLpNone)) {
+                arrive(&bars->ring_free[r % kLpRing]);
+                if (flags & kLpEnd) break;
+                continue;
+            }
+            const int n = sl->n;
+            uint8_t *sp = smem + (c % kLpStages) * SH::STAGE;
+            wait(&bars->full[c % kLpStages], c / kLpStages);
+            if (c > 0) wait(&bars->d_done, c - 1u);
+            if (ok) {
+#pragma unroll 4
+                for (int x = tid - 320; x < C * NP; x += 64) {
+                    const int t = x / NP, pc = x % NP;
+                    const uint4 kk = *reinterpret_cast<const uint4 *>(sp + 8192 + tile_off(t, pc, 16384u));
+                    const uint32_t u[4] = {kk.x, kk.y, kk.z, kk.w};
+                    const float f = sl->inv[t];
+                    const bool in = t < n;
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t k2 = in ? u[z] : 0u;
+                        lc_split2(f * __uint_as_float(k2 << 16), f * __uint_as_float(k2 & 0xFFFF0000u), hi[z], mid[z], lo[z]);
+                    }
+                    uint8_t *dp = smem + SH::K + tile_off(t, pc, 8192u);
+                    *reinterpret_cast<uint4 *>(dp) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(dp + KB * 8192) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    *reinterpret_cast<uint4 *>(dp + 2 * KB * 8192) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                // rows of V behind the chunk meet zeros of P and K', so they must be finite
+                for (int x = tid - 320; x < (C - n) * NP; x += 64)
+                    *reinterpret_cast<uint4 *>(sp + SH::V + tile_off(n + x / NP, x % NP, 8192u)) = make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
+            }
+            arrive(&bars->k_ready);
+            arrive(&bars->ring_free[r % kLpRing]);
+            ++c;
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------- the scores
+        const int t = tid - 256;  // row
+        uint32_t c = 0;
+#pragma unroll 1
+        for (uint32_t r = 0; ok; ++r) {
+            wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            const LpSlot *sl = ring + r % kLpRing;
+            const int flags = ok ? sl->flags : kLpEnd;
+            if (flags & (kLpEnd | kLpNone)) {
+                arrive(&bars->ring_free[r % kLpRing]);
+                if (flags & kLpEnd) break;
+                continue;
+            }
+            wait(&bars->qk_done, c);
+            tc_fence_after();
+            uint32_t v[4][16];
+            tmem_ld16_async(tlane + kLpQK, v[0]);
+            tmem_ld16_async(tlane + kLpQK + 16u, v[1]);
+            if (warp == 9) {
+                tmem_ld16_async(tlane + kLpQK + 32u, v[2]);
+                tmem_ld16_async(tlane + kLpQK + 48u, v[3]);
+                tmem_ld_wait(v[2]);
+                tmem_ld_wait(v[3]);
+            }
+            tmem_ld_wait(v[0]);
+            tmem_ld_wait(v[1]);
+            tc_fence_before();
+            arrive(&bars->qk_free);
+            if (c > 0) wait(&bars->o_done[(c - 1u) & 1u], (c - 1u) / 2u);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (b < 2 || warp == 9) {
+#pragma unroll
+                    for (int y = 0; y < 16; y += 8) {
+                        const int s0 = 16 * b + y;
+                        const float4 f0 = *reinterpret_cast<const float4 *>(sl->inv + s0);
+                        const float4 f1 = *reinterpret_cast<const float4 *>(sl->inv + s0 + 4);
+                        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                        uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float x0 = s0 + 2 * z <= t ? __uint_as_float(v[b][y + 2 * z]) * f[2 * z] : 0.f;
+                            const float x1 = s0 + 2 * z + 1 <= t ? __uint_as_float(v[b][y + 2 * z + 1]) * f[2 * z + 1] : 0.f;
+                            lc_split2(x0, x1, hi[z], mid[z], lo[z]);
+                        }
+                        uint8_t *o = smem + SH::P + tile_off(t, s0 >> 3, 0u);
+                        *reinterpret_cast<uint4 *>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(o + 8192) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                        *reinterpret_cast<uint4 *>(o + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+            fence_async_smem();
+            arrive(&bars->p_ready);
+            arrive(&bars->ring_free[r % kLpRing]);
+            ++c;
+        }
+    } else if ((warp & 3) < D / 32) {
+        // -------------------------------------------------------- the state
+        const int j = 32 * (warp & 3) + lane, half = warp >> 2;
+        const int st = tid - (D == 64 && half ? 64 : 0);  // index among the state threads
+        constexpr int NS = SH::SW * 32;
+        float S[HD];
+#pragma unroll
+        for (int x = 0; x < HD; ++x) S[x] = 0.f;
+        uint32_t c = 0;
+        int pend = -1;  // ring slot of a chunk whose outputs are to be written
+        int w = 0;
+        auto write_out = [&]() {  // outputs of chunk c - 1
+            const LpSlot *sl = ring + pend;
+            const uint32_t i = c - 1u;
+            wait(&bars->o_done[i & 1u], i / 2u);
+            tc_fence_after();
+            uint32_t v[2][16];
+            tmem_ld16_async(tlane + kLpO + 64u * (i & 1u) + 32u * half, v[0]);
+            tmem_ld16_async(tlane + kLpO + 64u * (i & 1u) + 32u * half + 16u, v[1]);
+            tmem_ld_wait(v[0]);
+            tmem_ld_wait(v[1]);
+            tc_fence_before();
+            arrive(&bars->o_free[i & 1u]);
+            if (A.out && ok) {
+                const int row = sl->w / A.map.heads, hh = sl->w - row * A.map.heads;
+                const int left = sl->n - 32 * half;
+                float *o = A.out + lin_v_row(A, row, hh, sl->t0 + 32 * half) * D + j;
+                const size_t step = (size_t)A.map.heads * D;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int y = 0; y < 16; y += 4) {
+                        const float4 g = *reinterpret_cast<const float4 *>(sl->G + 32 * half + 16 * b + y);
+                        const float gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            if (16 * b + y + z < left) *o = __uint_as_float(v[b][y + z]) * gg[z];
+                            o += step;
+                        }
+                    }
+            }
+            arrive(&bars->ring_free[pend]);
+            pend = -1;
+        };
+#pragma unroll 1
+        for (uint32_t r = 0; ok; ++r) {
+            wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            const LpSlot *sl = ring + r % kLpRing;
+            const int flags = ok ? sl->flags : kLpEnd;
+            if (flags & kLpEnd) break;
+            w = sl->w;
+            if (flags & kLpFirst) {
+                const int bi = A.map.blob(w);
+                const float *src = nullptr;
+                if (!(flags & kLpNone) || (flags & kLpFinal)) {
+                    if (A.nseg > 1) src = A.ws_S + ((size_t)w * A.nseg + sl->seg) * (D * D);
+                    else if (A.cont) src = reinterpret_cast<const float *>(A.state + (size_t)bi * A.L.blob + kHdrBytes);
+                    else if (A.S0) src = A.S0 + (size_t)w * (D * D);
+                }
+                const float f = (flags & kLpNone) ? 1.f : sl->a_first;
+#pragma unroll
+                for (int x = 0; x < HD; ++x) S[x] = src ? f * src[(size_t)(HD * half + x) * D + j] : 0.f;
+            }
+            if (!(flags & kLpNone)) {
+                // ---- S^T in three pieces (pairs of key channels)
+                if (c > 0) wait(&bars->y_done, c - 1u);
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < HD; x += 32) {
+                    uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) lc_split2(S[x + 2 * y], S[x + 2 * y + 1], hi[y], mid[y], lo[y]);
+                    const uint32_t at = tlane + kLpSp + (uint32_t)(half * (HD / 2) + x / 2);
+                    tmem_st16u(at, hi);
+                    tmem_st16u(at + HD, mid);
+                    tmem_st16u(at + 2 * HD, lo);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                arrive(&bars->s_ready);
+                if (pend >= 0) write_out();
+                // ---- S' = g (S + V^T K')
+                wait(&bars->d_done, c);
+                tc_fence_after();
+                const float g = sl->g_next;
+#pragma unroll
+                for (int x = 0; x < HD; x += 32) {
+                    uint32_t v0[16], v1[16];
+                    tmem_ld16_async(tlane + kLpD + (uint32_t)(HD * half + x), v0);
+                    tmem_ld16_async(tlane + kLpD + (uint32_t)(HD * half + x + 16), v1);
+                    tmem_ld_wait(v0);
+                    tmem_ld_wait(v1);
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        S[x + y] = g * (S[x + y] + __uint_as_float(v0[y]));
+                        S[x + 16 + y] = g * (S[x + 16 + y] + __uint_as_float(v1[y]));
+                    }
+                }
+                tc_fence_before();
+                arrive(&bars->d_free);
+                ++c;
+                pend = (int)(r % kLpRing);
+            }
+            if ((flags & kLpLast) && ok) {
+                const int row = w / A.map.heads, hh = w - row * A.map.heads;
+                const int t_done = sl->t0 + sl->n, t_end = sl->zero_end;
+                if (flags & kLpFinal) {  // the prompt's end
+                    uint8_t *blob = A.state + (size_t)A.map.blob(w) * A.L.blob;
+                    float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + (size_t)(HD * half) * D + j;
+#pragma unroll
+                    for (int x = 0; x < HD; ++x) dst[(size_t)x * D] = S[x];
+                    if (tid == 0) lin_write_header(blob, A.cont, (flags & kLpBad) != 0);
+                }
+                if (A.out)  // no outputs past it
+                    for (int x = st; x < (t_end - t_done) * (D / 4); x += NS)
+                        *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, t_done + x / (D / 4)) * D +
+                                                    4 * (x % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (flags & kLpNone) arrive(&bars->ring_free[r % kLpRing]);
+        }
+        if (ok && pend >= 0) write_out();
+        if (!ok && lane == 0) {  // this item and those behind it are not done
+            for (int x = blockIdx.x; x < items; x += gridDim.x) {
+                const int bi = x / A.nseg >= w ? A.map.blob(x / A.nseg) : -1;
+                if (bi >= 0) set_status(A.state + (size_t)bi * A.L.blob, LQ_DEV_TIMEOUT);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) tmem_dealloc(tmem, 512u);
+}
+
+}  // namespace lq
