@@ -183,7 +183,7 @@ lq_status prefill_rows(const lq_config &c, void *state, const int32_t *slots, in
     if (tokens < 0 || (flags & ~LQ_PREFILL_CONTINUE)) return LQ_ERR_INVALID_ARG;
     if ((flags & LQ_PREFILL_CONTINUE) && S0) return LQ_ERR_INVALID_ARG;
     if ((int64_t)rows * (tokens > 0 ? tokens : 1) * c.num_heads > 0x7FFFFFFF) return LQ_ERR_UNSUPPORTED;
-    if ((int64_t)rows * c.num_heads > 0x7FFFFFFF / 16) return LQ_ERR_UNSUPPORTED;
+    if ((int64_t)rows * c.num_heads > 0x7FFFFFFF / 16 || c.num_heads > 0x7FFFFFFF / 128) return LQ_ERR_UNSUPPORTED;
     if (rows > 0 && tokens > 0 && (!q || !k || !v || !decay)) return LQ_ERR_INVALID_ARG;
     if (!aligned(state, 256) || !aligned(slots, 4) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
         !aligned(decay, 4) || !aligned(out, 16) || !aligned(S0, 16) || !aligned(lengths, 4) || !aligned(workspace, 16))

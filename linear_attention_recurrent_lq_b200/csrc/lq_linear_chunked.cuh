@@ -56,9 +56,13 @@ struct LcShape {
     static constexpr uint32_t SMEM = SMEM_USED > 90u * 1024u ? SMEM_USED : 90u * 1024u;
 };
 
-__device__ __forceinline__ uint64_t lc_desc(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory matrix descriptors (128-byte swizzle, 1024 bytes between
+// groups of eight rows) differ in their low word only: the address and, for an
+// operand read along its rows, the distance of its 64-element blocks.  The
+// issuing thread adds to that word; the high word is a constant.
+constexpr uint32_t kLcDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t lc_desc(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
 }
 
 // D in FP32, A and B in bf16; a bit per operand read along its rows (MN-major).
@@ -67,20 +71,29 @@ __host__ __device__ constexpr uint32_t lc_idesc(int M, int N, int a_mn, int b_mn
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void lc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void lc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kLcDescHi)
         : "memory");
 }
 
-__device__ __forceinline__ void lc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void lc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kLcDescHi)
         : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool lc_elect() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -97,11 +110,12 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void lc_split2(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
     const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
     hi = __byte_perm(xb, yb, 0x7632);
-    const float x1 = x - __uint_as_float(xb & 0xFFFF0000u), y1 = y - __uint_as_float(yb & 0xFFFF0000u);
-    const uint32_t xm = __float_as_uint(x1), ym = __float_as_uint(y1);
+    const float2 minus = make_float2(-1.f, -1.f);
+    const float2 one = __ffma2_rn(make_float2(__uint_as_float(xb & 0xFFFF0000u), __uint_as_float(yb & 0xFFFF0000u)), minus, make_float2(x, y));
+    const uint32_t xm = __float_as_uint(one.x), ym = __float_as_uint(one.y);
     mid = __byte_perm(xm, ym, 0x7632);
-    const float x2 = x1 - __uint_as_float(xm & 0xFFFF0000u), y2 = y1 - __uint_as_float(ym & 0xFFFF0000u);
-    lo = __byte_perm(__float_as_uint(x2), __float_as_uint(y2), 0x7632);
+    const float2 two = __ffma2_rn(make_float2(__uint_as_float(xm & 0xFFFF0000u), __uint_as_float(ym & 0xFFFF0000u)), minus, one);
+    lo = __byte_perm(__float_as_uint(two.x), __float_as_uint(two.y), 0x7632);
 }
 
 template <int D, bool PARTIAL>

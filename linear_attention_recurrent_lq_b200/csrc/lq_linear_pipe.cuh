@@ -16,21 +16,20 @@
 // exactly, multiplied smallest first, and summed in FP32.
 //
 // One CTA per SM walks the work items (a head, or a segment of a prompt cut
-// along time) b, b + grid, ... as one stream of chunks.  Its warps:
-//   0 .. 7   the state, in registers (lane = value channel, the two groups of
-//            four warps take half of the key channels each): its three pieces
-//            to tensor memory as an A operand, the outputs from tensor memory
-//            to global memory, the update
-//   8, 9     the scores: from tensor memory, times 1 / G, masked, three pieces
-//            to shared memory
-//   10, 11   k / G in three pieces to shared memory
-//   12       one thread issues every product, in the order Q K^T of chunk c,
+// along time) b, b + grid, ... as one stream of chunks.  The state is an FP32
+// accumulator in tensor memory (lane = value channel) onto which V^T K' is
+// summed.  The CTA's warps, one of each kind on every scheduler:
+//   0 .. 7   the state: scaled, and cut into the pieces of an A operand in
+//            tensor memory; read from and written to global memory
+//   8 .. 11  the outputs, from tensor memory to global memory
+//   12 .. 15 K' = k / G in three pieces to shared memory
+//   16, 17, 21  the scores Q K^T, a block of 32 x 32 each: from tensor memory,
+//            times 1 / G, masked, in three pieces to shared memory
+//   18       one thread issues every product, in the order Q K^T of chunk c,
 //            V^T P^T of c - 1, V^T K' of c, S^T Q^T of c
-//   13       the feeder: gates and their products, the chunk's bounds, and the
+//   19       the feeder: gates and their products, the chunk's bounds, and the
 //            TMA loads, up to three chunks ahead
-// They meet in mbarriers only.  Bound by HBM at 1284 bytes per token and head
-// (d = 128): 3440 clocks per chunk and SM, next to about 2500 of tensor time
-// and 2300 issue slots per scheduler.
+// They meet in mbarriers only.
 #pragma once
 
 #include <cuda.h>
@@ -39,12 +38,12 @@
 
 namespace lq {
 
-constexpr int kLpThreads = 14 * 32;
+constexpr int kLpThreads = 24 * 32;
 constexpr int kLpStages = 3;   // chunks of q, k, v in shared memory
 constexpr int kLpRing = 4;     // chunk descriptions
 constexpr float kLpMinGate = 0x1p-64f;
-// tensor memory: Q K^T | O^T, two | S pieces | V^T K'
-constexpr uint32_t kLpQK = 0, kLpO = 64, kLpSp = 192, kLpD = 384;
+// tensor memory: Q K^T | O^T, two | S pieces | S
+constexpr uint32_t kLpQK = 0, kLpO = 64, kLpSp = 192, kLpS = 384;
 
 enum : int { kLpFirst = 1, kLpLast = 2, kLpFinal = 4, kLpBad = 8, kLpNone = 16, kLpEnd = 32 };
 
@@ -63,12 +62,13 @@ struct LpShape {
     static constexpr uint32_t P = kLpStages * STAGE, K = P + 3u * 8192u, RING = K + 3u * KB * 8192u;
     static constexpr uint32_t BAR = RING + kLpRing * (uint32_t)sizeof(LpSlot);
     static constexpr uint32_t SMEM = BAR + 256u + 1024u;
-    static constexpr int SW = D / 16;  // warps that hold state: all eight, or the four whose lanes are < 64
+    // state and output warps at work: all, or those whose lanes are < 64
+    static constexpr int SW = D / 16, OW = D / 32;
 };
 
 struct LpBars {
     uint64_t full[kLpStages], empty[kLpStages], ring_full[kLpRing], ring_free[kLpRing];
-    uint64_t qk_done, qk_free, p_ready, k_ready, s_ready, y_done, d_done, d_free, o_done[2], o_free[2];
+    uint64_t qk_done, qk_free, p_ready, k_ready, s_ready, y_done, d_done, o_done[2], o_free[2];
     uint32_t tmem, fail;
 };
 static_assert(sizeof(LpBars) <= 256, "barrier space");
@@ -98,6 +98,12 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
                  ::"memory");
 }
 
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kLpThreads, 1)
     lin_pipe_kernel(const LinArgs A, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -119,25 +125,24 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         }
         for (int i = 0; i < kLpRing; ++i) {
             mbar_init(&bars->ring_full[i], 1);
-            mbar_init(&bars->ring_free[i], SH::SW + 5);  // state, score and key warps, the issuer
+            mbar_init(&bars->ring_free[i], SH::SW + SH::OW + 8);  // key, score and issuing warps too
         }
         mbar_init(&bars->qk_done, 1);
-        mbar_init(&bars->qk_free, 2);
-        mbar_init(&bars->p_ready, 2);
-        mbar_init(&bars->k_ready, 2);
+        mbar_init(&bars->qk_free, 3);
+        mbar_init(&bars->p_ready, 3);
+        mbar_init(&bars->k_ready, 4);
         mbar_init(&bars->s_ready, SH::SW);
         mbar_init(&bars->y_done, 1);
         mbar_init(&bars->d_done, 1);
-        mbar_init(&bars->d_free, SH::SW);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->o_done[i], 1);
-            mbar_init(&bars->o_free[i], SH::SW);
+            mbar_init(&bars->o_free[i], SH::OW);
         }
         bars->fail = 0u;
         fence_mbar_init();
     }
     pdl_wait();
-    if (warp == 12) tmem_alloc(&bars->tmem, 512u);  // after the wait: a kernel still running may need it
+    if (warp == 18) tmem_alloc(&bars->tmem, 512u);  // after the wait: a kernel still running may need it
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
@@ -148,7 +153,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 
     bool ok = true;  // false: a wait gave up; every role then leaves
     auto wait = [&](uint64_t *b, uint32_t phase) {
-        if (!mbar_wait_bounded(b, phase & 1u)) ok = false;
+        // the first try in line: most waits end there
+        if (!mbar_try_wait(b, phase & 1u) && !mbar_wait_bounded(b, phase & 1u)) ok = false;
     };
     auto arrive = [&](uint64_t *b) {  // one arrival per warp, after all its lanes
         __syncwarp();
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
     };
 
-    if (warp == 13) {
+    if (warp == 19) {
         // ------------------------------------------------------- the feeder
         uint32_t r = 0, c = 0;
         auto slot_wait = [&]() -> LpSlot * {
@@ -227,7 +233,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 
                 const uint32_t st = c % kLpStages;
                 if (c >= kLpStages) wait(&bars->empty[st], c / kLpStages - 1u);
-                if (lane == 0 && ok) {
+                if (ok && lc_elect()) {
                     uint8_t *sp = smem + st * SH::STAGE;
                     mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
 #pragma unroll
@@ -266,7 +272,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         // what has been asked for lands before the CTA leaves
         for (uint32_t i = c > kLpStages ? c - kLpStages : 0u; i < c; ++i)
             mbar_wait_bounded(&bars->full[i % kLpStages], (i / kLpStages) & 1u);
-    } else if (warp == 12) {
+    } else if (warp == 18) {
         // ------------------------------------------------------- the issuer
         constexpr uint32_t id64 = lc_idesc(128, 64, 0, 0), idpv = lc_idesc(128, 64, 1, 0), idpv2 = lc_idesc(128, 32, 1, 0),
                            idd = lc_idesc(128, D, 1, 1);
@@ -274,18 +280,18 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         uint32_t c = 0;
         auto pv = [&](uint32_t i) {  // O^T += V^T P^T of chunk i
             wait(&bars->p_ready, i);
-            if (lane == 0 && ok) {
+            if (ok && lc_elect()) {
                 tc_fence_after();
-                const uint32_t vb = base + (i % kLpStages) * SH::STAGE + SH::V, o = tmem + kLpO + 64u * (i & 1u);
+                const uint32_t vb = lc_desc(base + (i % kLpStages) * SH::STAGE + SH::V, vlbo), o = tmem + kLpO + 64u * (i & 1u);
 #pragma unroll
                 for (int x = 2; x >= 0; --x) {
-                    const uint32_t pb = base + SH::P + (uint32_t)x * 8192u;
+                    const uint32_t pb = lc_desc(base + SH::P, 16u) + (uint32_t)x * 512u;
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)  // tokens 32 .. reach rows 32 .. only
                         if (ks < 2)
-                            lc_mma_ss(o, lc_desc(vb + ks * 2048u, vlbo), lc_desc(pb + ks * 32u, 16u), idpv, 1u);
+                            lc_mma_ss(o, vb + ks * 128u, pb + ks * 2u, idpv, 1u);
                         else
-                            lc_mma_ss(o + 32u, lc_desc(vb + ks * 2048u, vlbo), lc_desc(pb + 4096u + ks * 32u, 16u), idpv2, 1u);
+                            lc_mma_ss(o + 32u, vb + ks * 128u, pb + 256u + ks * 2u, idpv2, 1u);
                 }
                 umma_commit(&bars->o_done[i & 1u]);
                 umma_commit(&bars->empty[i % kLpStages]);
@@ -302,40 +308,39 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             const uint32_t sb = base + (c % kLpStages) * SH::STAGE;
             wait(&bars->full[c % kLpStages], c / kLpStages);
             if (c > 0) wait(&bars->qk_free, c - 1u);
-            if (lane == 0 && ok) {  // Q K^T; rows 64 .. 127 (K K^T) are not used
+            if (ok && lc_elect()) {  // Q K^T; rows 64 .. 127 (K K^T) are not used
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t o = sb + (uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u;
-                    lc_mma_ss(tmem + kLpQK, lc_desc(o, 16u), lc_desc(o + 8192u, 16u), id64, ks > 0);
+                    const uint32_t o = lc_desc(sb, 16u) + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u;
+                    lc_mma_ss(tmem + kLpQK, o, o + 512u, id64, ks > 0);
                 }
                 umma_commit(&bars->qk_done);
             }
             __syncwarp();
             if (c > 0) pv(c - 1u);
             wait(&bars->k_ready, c);
-            if (c > 0) wait(&bars->d_free, c - 1u);
-            if (lane == 0 && ok) {  // V^T K'
+            wait(&bars->s_ready, c);
+            if (ok && lc_elect()) {  // S += V^T K'
                 tc_fence_after();
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks)
-                        lc_mma_ss(tmem + kLpD, lc_desc(sb + SH::V + ks * 2048u, vlbo),
-                                  lc_desc(base + SH::K + (uint32_t)x * (KB * 8192u) + ks * 2048u, 8192u), idd, x < 2 || ks > 0);
+                        lc_mma_ss(tmem + kLpS, lc_desc(sb + SH::V, vlbo) + ks * 128u,
+                                  lc_desc(base + SH::K, 8192u) + (uint32_t)x * (KB * 512u) + ks * 128u, idd, 1u);
                 umma_commit(&bars->d_done);
             }
             __syncwarp();
-            wait(&bars->s_ready, c);
             if (c > 1) wait(&bars->o_free[c & 1u], c / 2u - 1u);
-            if (lane == 0 && ok) {  // S^T Q^T
+            if (ok && lc_elect()) {  // S^T Q^T
                 tc_fence_after();
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
                         lc_mma_ts(tmem + kLpO + 64u * (c & 1u), tmem + kLpSp + (uint32_t)(x * HD + 8 * ks),
-                                  lc_desc(sb + (uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u, 16u), id64,
+                                  lc_desc(sb, 16u) + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u, id64,
                                   x < 2 || ks > 0);
                 umma_commit(&bars->y_done);
             }
@@ -345,9 +350,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         if (c > 0 && ok) pv(c - 1u);
         // every product has ended before tensor memory is given back
         if (c > 0) mbar_wait_bounded(&bars->o_done[(c - 1u) & 1u], ((c - 1u) / 2u) & 1u);
-    } else if (warp >= 10) {
+    } else if (warp >= 12 && warp < 16) {
         // ------------------------------------------------- k / G, in pieces
-        constexpr int NP = 8 * KB;
+        constexpr int NP = 8 * KB, NT = 128;
+        const int kt = tid - 384;
         uint32_t c = 0;
 #pragma unroll 1
         for (uint32_t r = 0; ok; ++r) {
@@ -364,18 +370,18 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             wait(&bars->full[c % kLpStages], c / kLpStages);
             if (c > 0) wait(&bars->d_done, c - 1u);
             if (ok) {
-#pragma unroll 4
-                for (int x = tid - 320; x < C * NP; x += 64) {
+#pragma unroll 2
+                for (int x = kt; x < C * NP; x += NT) {
                     const int t = x / NP, pc = x % NP;
-                    const uint4 kk = *reinterpret_cast<const uint4 *>(sp + 8192 + tile_off(t, pc, 16384u));
+                    uint4 kk = make_uint4(0u, 0u, 0u, 0u);  // rows behind the chunk
+                    if (t < n) kk = *reinterpret_cast<const uint4 *>(sp + 8192 + tile_off(t, pc, 16384u));
                     const uint32_t u[4] = {kk.x, kk.y, kk.z, kk.w};
-                    const float f = sl->inv[t];
-                    const bool in = t < n;
+                    const float2 f = make_float2(sl->inv[t], sl->inv[t]);
                     uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
-                        const uint32_t k2 = in ? u[z] : 0u;
-                        lc_split2(f * __uint_as_float(k2 << 16), f * __uint_as_float(k2 & 0xFFFF0000u), hi[z], mid[z], lo[z]);
+                        const float2 kf = __fmul2_rn(f, make_float2(__uint_as_float(u[z] << 16), __uint_as_float(u[z] & 0xFFFF0000u)));
+                        lc_split2(kf.x, kf.y, hi[z], mid[z], lo[z]);
                     }
                     uint8_t *dp = smem + SH::K + tile_off(t, pc, 8192u);
                     *reinterpret_cast<uint4 *>(dp) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     *reinterpret_cast<uint4 *>(dp + 2 * KB * 8192) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 // rows of V behind the chunk meet zeros of P and K', so they must be finite
-                for (int x = tid - 320; x < (C - n) * NP; x += 64)
+                for (int x = kt; x < (C - n) * NP; x += NT)
                     *reinterpret_cast<uint4 *>(sp + SH::V + tile_off(n + x / NP, x % NP, 8192u)) = make_uint4(0u, 0u, 0u, 0u);
                 fence_async_smem();
             }
@@ -391,9 +397,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             arrive(&bars->ring_free[r % kLpRing]);
             ++c;
         }
-    } else if (warp >= 8) {
+    } else if (warp == 16 || warp == 17 || warp == 21) {
         // ------------------------------------------------------- the scores
-        const int t = tid - 256;  // row
+        const int t = 32 * (warp & 3) + lane, c0 = warp == 21 ? 32 : 0;  // row, first column
+        const int diag = warp == 17 ? 32 : lane;  // last column of the block that the row sees
         uint32_t c = 0;
 #pragma unroll 1
         for (uint32_t r = 0; ok; ++r) {
@@ -407,98 +414,111 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             }
             wait(&bars->qk_done, c);
             tc_fence_after();
-            uint32_t v[4][16];
-            tmem_ld16_async(tlane + kLpQK, v[0]);
-            tmem_ld16_async(tlane + kLpQK + 16u, v[1]);
-            if (warp == 9) {
-                tmem_ld16_async(tlane + kLpQK + 32u, v[2]);
-                tmem_ld16_async(tlane + kLpQK + 48u, v[3]);
-                tmem_ld_wait(v[2]);
-                tmem_ld_wait(v[3]);
-            }
+            uint32_t v[2][16];
+            tmem_ld16_async(tlane + kLpQK + (uint32_t)c0, v[0]);
+            tmem_ld16_async(tlane + kLpQK + (uint32_t)c0 + 16u, v[1]);
             tmem_ld_wait(v[0]);
             tmem_ld_wait(v[1]);
             tc_fence_before();
             arrive(&bars->qk_free);
             if (c > 0) wait(&bars->o_done[(c - 1u) & 1u], (c - 1u) / 2u);
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (b < 2 || warp == 9) {
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int y = 0; y < 16; y += 8) {
-                        const int s0 = 16 * b + y;
-                        const float4 f0 = *reinterpret_cast<const float4 *>(sl->inv + s0);
-                        const float4 f1 = *reinterpret_cast<const float4 *>(sl->inv + s0 + 4);
-                        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                        uint32_t hi[4], mid[4], lo[4];
+                for (int y = 0; y < 16; y += 8) {
+                    const int s0 = 16 * b + y;  // inside the block
+                    const float4 f0 = *reinterpret_cast<const float4 *>(sl->inv + c0 + s0);
+                    const float4 f1 = *reinterpret_cast<const float4 *>(sl->inv + c0 + s0 + 4);
+                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                    uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const float x0 = s0 + 2 * z <= t ? __uint_as_float(v[b][y + 2 * z]) * f[2 * z] : 0.f;
-                            const float x1 = s0 + 2 * z + 1 <= t ? __uint_as_float(v[b][y + 2 * z + 1]) * f[2 * z + 1] : 0.f;
-                            lc_split2(x0, x1, hi[z], mid[z], lo[z]);
-                        }
-                        uint8_t *o = smem + SH::P + tile_off(t, s0 >> 3, 0u);
-                        *reinterpret_cast<uint4 *>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(o + 8192) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                        *reinterpret_cast<uint4 *>(o + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int z = 0; z < 4; ++z) {
+                        const float2 x2 = __fmul2_rn(make_float2(__uint_as_float(v[b][y + 2 * z]), __uint_as_float(v[b][y + 2 * z + 1])),
+                                                     make_float2(f[2 * z], f[2 * z + 1]));
+                        lc_split2(s0 + 2 * z <= diag ? x2.x : 0.f, s0 + 2 * z + 1 <= diag ? x2.y : 0.f, hi[z], mid[z], lo[z]);
                     }
+                    uint8_t *o = smem + SH::P + tile_off(t, (c0 + s0) >> 3, 0u);
+                    *reinterpret_cast<uint4 *>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(o + 8192) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    *reinterpret_cast<uint4 *>(o + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             fence_async_smem();
             arrive(&bars->p_ready);
             arrive(&bars->ring_free[r % kLpRing]);
             ++c;
         }
-    } else if ((warp & 3) < D / 32) {
+    } else if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------------ the outputs
+        if ((warp & 3) < D / 32) {
+            const int j = 32 * (warp & 3) + lane;
+            constexpr int NT = SH::OW * 32;
+            const uint32_t step = (uint32_t)A.map.heads * D;  // < 2^31
+            uint32_t c = 0;
+#pragma unroll 1
+            for (uint32_t r = 0; ok; ++r) {
+                wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+                const LpSlot *sl = ring + r % kLpRing;
+                const int flags = ok ? sl->flags : kLpEnd;
+                if (flags & kLpEnd) {
+                    arrive(&bars->ring_free[r % kLpRing]);
+                    break;
+                }
+                const int row = sl->w / A.map.heads, hh = sl->w - row * A.map.heads, n = sl->n;
+                if (!(flags & kLpNone)) {
+                    float *o = A.out + lin_v_row(A, row, hh, sl->t0) * D + j;
+                    wait(&bars->o_done[c & 1u], c / 2u);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < C; x += 32) {
+                        uint32_t v[2][16];
+                        tmem_ld16_async(tlane + kLpO + 64u * (c & 1u) + (uint32_t)x, v[0]);
+                        tmem_ld16_async(tlane + kLpO + 64u * (c & 1u) + (uint32_t)x + 16u, v[1]);
+                        tmem_ld_wait(v[0]);
+                        tmem_ld_wait(v[1]);
+                        if (x + 32 >= C) {
+                            tc_fence_before();
+                            arrive(&bars->o_free[c & 1u]);
+                        }
+                        if (A.out && ok)
+#pragma unroll
+                            for (int y = 0; y < 32; y += 4) {
+                                const float4 g = *reinterpret_cast<const float4 *>(sl->G + x + y);
+                                const float gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    if (x + y + z < n)
+                                        o[(uint64_t)(uint32_t)(y + z) * step] = __uint_as_float(v[(y + z) >> 4][(y + z) & 15]) * gg[z];
+                            }
+                        o += (size_t)32 * step;
+                    }
+                    ++c;
+                }
+                if ((flags & kLpLast) && A.out && ok)  // no outputs past the prompt's end
+                    for (int x = tid - 256; x < (sl->zero_end - sl->t0 - n) * (D / 4); x += NT)
+                        *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, sl->t0 + n + x / (D / 4)) * D +
+                                                    4 * (x % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
+                arrive(&bars->ring_free[r % kLpRing]);
+            }
+        }
+    } else if (warp < 8 && (warp & 3) < D / 32) {
         // -------------------------------------------------------- the state
         const int j = 32 * (warp & 3) + lane, half = warp >> 2;
-        const int st = tid - (D == 64 && half ? 64 : 0);  // index among the state threads
-        constexpr int NS = SH::SW * 32;
-        float S[HD];
-#pragma unroll
-        for (int x = 0; x < HD; ++x) S[x] = 0.f;
+        const uint32_t ts = tlane + kLpS + (uint32_t)(HD * half), tp = tlane + kLpSp + (uint32_t)(HD / 2 * half);
         uint32_t c = 0;
-        int pend = -1;  // ring slot of a chunk whose outputs are to be written
+        float g = 1.f;  // scale of the accumulator
         int w = 0;
-        auto write_out = [&]() {  // outputs of chunk c - 1
-            const LpSlot *sl = ring + pend;
-            const uint32_t i = c - 1u;
-            wait(&bars->o_done[i & 1u], i / 2u);
-            tc_fence_after();
-            uint32_t v[2][16];
-            tmem_ld16_async(tlane + kLpO + 64u * (i & 1u) + 32u * half, v[0]);
-            tmem_ld16_async(tlane + kLpO + 64u * (i & 1u) + 32u * half + 16u, v[1]);
-            tmem_ld_wait(v[0]);
-            tmem_ld_wait(v[1]);
-            tc_fence_before();
-            arrive(&bars->o_free[i & 1u]);
-            if (A.out && ok) {
-                const int row = sl->w / A.map.heads, hh = sl->w - row * A.map.heads;
-                const int left = sl->n - 32 * half;
-                float *o = A.out + lin_v_row(A, row, hh, sl->t0 + 32 * half) * D + j;
-                const size_t step = (size_t)A.map.heads * D;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int y = 0; y < 16; y += 4) {
-                        const float4 g = *reinterpret_cast<const float4 *>(sl->G + 32 * half + 16 * b + y);
-                        const float gg[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            if (16 * b + y + z < left) *o = __uint_as_float(v[b][y + z]) * gg[z];
-                            o += step;
-                        }
-                    }
-            }
-            arrive(&bars->ring_free[pend]);
-            pend = -1;
-        };
 #pragma unroll 1
         for (uint32_t r = 0; ok; ++r) {
             wait(&bars->ring_full[r % kLpRing], r / kLpRing);
             const LpSlot *sl = ring + r % kLpRing;
             const int flags = ok ? sl->flags : kLpEnd;
-            if (flags & kLpEnd) break;
+            if (flags & kLpEnd) {
+                arrive(&bars->ring_free[r % kLpRing]);
+                break;
+            }
             w = sl->w;
+            if (c > 0) wait(&bars->d_done, c - 1u);
+            tc_fence_after();
             if (flags & kLpFirst) {
                 const int bi = A.map.blob(w);
                 const float *src = nullptr;
@@ -507,78 +527,84 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     else if (A.cont) src = reinterpret_cast<const float *>(A.state + (size_t)bi * A.L.blob + kHdrBytes);
                     else if (A.S0) src = A.S0 + (size_t)w * (D * D);
                 }
-                const float f = (flags & kLpNone) ? 1.f : sl->a_first;
+                if (src) src += (size_t)(HD * half) * D + j;
+#pragma unroll 1
+                for (int x = 0; x < HD; x += 32) {
+                    uint32_t v[32];
 #pragma unroll
-                for (int x = 0; x < HD; ++x) S[x] = src ? f * src[(size_t)(HD * half + x) * D + j] : 0.f;
+                    for (int y = 0; y < 32; ++y) v[y] = src ? __float_as_uint(src[(size_t)(x + y) * D]) : 0u;
+                    uint32_t lo[16], up[16];
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        lo[y] = v[y];
+                        up[y] = v[16 + y];
+                    }
+                    tmem_st16u(ts + (uint32_t)x, lo);
+                    tmem_st16u(ts + (uint32_t)x + 16u, up);
+                }
+                tmem_st_wait();
+                g = (flags & kLpNone) ? 1.f : sl->a_first;
             }
             if (!(flags & kLpNone)) {
-                // ---- S^T in three pieces (pairs of key channels)
+                // ---- S scaled, and S^T in three pieces (pairs of key channels)
                 if (c > 0) wait(&bars->y_done, c - 1u);
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < HD; x += 32) {
-                    uint32_t hi[16], mid[16], lo[16];
+                    uint32_t v[2][16];
+                    tmem_ld16_async(ts + (uint32_t)x, v[0]);
+                    tmem_ld16_async(ts + (uint32_t)x + 16u, v[1]);
+                    tmem_ld_wait(v[0]);
+                    tmem_ld_wait(v[1]);
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) lc_split2(S[x + 2 * y], S[x + 2 * y + 1], hi[y], mid[y], lo[y]);
-                    const uint32_t at = tlane + kLpSp + (uint32_t)(half * (HD / 2) + x / 2);
-                    tmem_st16u(at, hi);
-                    tmem_st16u(at + HD, mid);
-                    tmem_st16u(at + 2 * HD, lo);
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const float2 s2 = __fmul2_rn(make_float2(g, g), make_float2(__uint_as_float(v[b][2 * y]), __uint_as_float(v[b][2 * y + 1])));
+                            v[b][2 * y] = __float_as_uint(s2.x);
+                            v[b][2 * y + 1] = __float_as_uint(s2.y);
+                            lc_split2(s2.x, s2.y, hi[y], mid[y], lo[y]);
+                        }
+                        tmem_st16u(ts + (uint32_t)(x + 16 * b), v[b]);
+                        tmem_st8u(tp + (uint32_t)(x / 2 + 8 * b), hi);
+                        tmem_st8u(tp + HD + (uint32_t)(x / 2 + 8 * b), mid);
+                        tmem_st8u(tp + 2 * HD + (uint32_t)(x / 2 + 8 * b), lo);
+                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 arrive(&bars->s_ready);
-                if (pend >= 0) write_out();
-                // ---- S' = g (S + V^T K')
-                wait(&bars->d_done, c);
+                g = sl->g_next;
+                ++c;
+            }
+            if ((flags & kLpFinal) && ok) {  // the prompt's end
+                if (!(flags & kLpNone)) wait(&bars->d_done, c - 1u);
                 tc_fence_after();
-                const float g = sl->g_next;
+                uint8_t *blob = A.state + (size_t)A.map.blob(w) * A.L.blob;
+                float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + (size_t)(HD * half) * D + j;
+#pragma unroll 1
+                for (int x = 0; x < HD; x += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_async(ts + (uint32_t)x, v);
+                    tmem_ld_wait(v);
 #pragma unroll
-                for (int x = 0; x < HD; x += 32) {
-                    uint32_t v0[16], v1[16];
-                    tmem_ld16_async(tlane + kLpD + (uint32_t)(HD * half + x), v0);
-                    tmem_ld16_async(tlane + kLpD + (uint32_t)(HD * half + x + 16), v1);
-                    tmem_ld_wait(v0);
-                    tmem_ld_wait(v1);
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        S[x + y] = g * (S[x + y] + __uint_as_float(v0[y]));
-                        S[x + 16 + y] = g * (S[x + 16 + y] + __uint_as_float(v1[y]));
-                    }
+                    for (int y = 0; y < 16; ++y) dst[(size_t)(x + y) * D] = g * __uint_as_float(v[y]);
                 }
                 tc_fence_before();
-                arrive(&bars->d_free);
-                ++c;
-                pend = (int)(r % kLpRing);
+                if (tid == 0) lin_write_header(blob, A.cont, (flags & kLpBad) != 0);
             }
-            if ((flags & kLpLast) && ok) {
-                const int row = w / A.map.heads, hh = w - row * A.map.heads;
-                const int t_done = sl->t0 + sl->n, t_end = sl->zero_end;
-                if (flags & kLpFinal) {  // the prompt's end
-                    uint8_t *blob = A.state + (size_t)A.map.blob(w) * A.L.blob;
-                    float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + (size_t)(HD * half) * D + j;
-#pragma unroll
-                    for (int x = 0; x < HD; ++x) dst[(size_t)x * D] = S[x];
-                    if (tid == 0) lin_write_header(blob, A.cont, (flags & kLpBad) != 0);
-                }
-                if (A.out)  // no outputs past it
-                    for (int x = st; x < (t_end - t_done) * (D / 4); x += NS)
-                        *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, t_done + x / (D / 4)) * D +
-                                                    4 * (x % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            if (flags & kLpNone) arrive(&bars->ring_free[r % kLpRing]);
+            arrive(&bars->ring_free[r % kLpRing]);
         }
-        if (ok && pend >= 0) write_out();
-        if (!ok && lane == 0) {  // this item and those behind it are not done
+        if (!ok && lane == 0)  // this item and those behind it are not done
             for (int x = blockIdx.x; x < items; x += gridDim.x) {
                 const int bi = x / A.nseg >= w ? A.map.blob(x / A.nseg) : -1;
                 if (bi >= 0) set_status(A.state + (size_t)bi * A.L.blob, LQ_DEV_TIMEOUT);
             }
-        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) tmem_dealloc(tmem, 512u);
+    if (warp == 18) tmem_dealloc(tmem, 512u);
 }
 
 }  // namespace lq
