@@ -105,18 +105,22 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two FP32 values in three pairs of bf16 pieces (8 leading bits, the next 8,
-// the rest: cut off, not rounded, so the pieces add up to the value exactly).
+// Two FP32 values in three pairs of bf16 pieces: the 8 leading bits, the next
+// 8, the rest (cut off, not rounded), so that x = hi - mid + lo exactly.  The
+// middle piece comes out negated, because the subtraction that takes a bf16
+// half of a register as it is (no masks: 6.6 clocks of a scheduler a pair,
+// 9.6 with them) has it first; the products with it negate it back.
 __device__ __forceinline__ void lc_split2(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
-    hi = __byte_perm(xb, yb, 0x7632);
-    const float2 minus = make_float2(-1.f, -1.f);
-    const float2 one = __ffma2_rn(make_float2(__uint_as_float(xb & 0xFFFF0000u), __uint_as_float(yb & 0xFFFF0000u)), minus, make_float2(x, y));
-    const uint32_t xm = __float_as_uint(one.x), ym = __float_as_uint(one.y);
-    mid = __byte_perm(xm, ym, 0x7632);
-    const float2 two = __ffma2_rn(make_float2(__uint_as_float(xm & 0xFFFF0000u), __uint_as_float(ym & 0xFFFF0000u)), minus, one);
-    lo = __byte_perm(__float_as_uint(two.x), __float_as_uint(two.y), 0x7632);
+    float x1, y1, x2, y2;
+    hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tsub.rn.f32.bf16 %0, a, %3;\n\tsub.rn.f32.bf16 %1, b, %4;\n\t}"
+        : "=f"(x1), "=f"(y1) : "r"(hi), "f"(x), "f"(y));
+    mid = __byte_perm(__float_as_uint(x1), __float_as_uint(y1), 0x7632);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tsub.rn.f32.bf16 %0, a, %3;\n\tsub.rn.f32.bf16 %1, b, %4;\n\t}"
+        : "=f"(x2), "=f"(y2) : "r"(mid), "f"(x1), "f"(y1));
+    lo = __byte_perm(__float_as_uint(x2), __float_as_uint(y2), 0x7632);
 }
+constexpr uint32_t kLcNegA = 1u << 13, kLcNegB = 1u << 14;  // of the instruction descriptor
 
 template <int D, bool PARTIAL>
 __global__ void __launch_bounds__(kLcThreads, 2) lin_chunk_kernel(LinArgs A) {
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(kLcThreads, 2) lin_chunk_kernel(LinArgs A) {
                     for (int ks = 0; ks < D / 16; ++ks)
                         lc_mma_ts(tmem + kLcO, tmem + kLcR + (uint32_t)(x * HD + 8 * ks),
                                   lc_desc(base + SH::QK + (uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u, 16u),
-                                  id, x < 2 || ks > 0);
+                                  id | (x == 1 ? kLcNegA : 0u), x < 2 || ks > 0);
                 umma_commit(&bar[0]);
             }
         }
@@ -389,7 +393,8 @@ __global__ void __launch_bounds__(kLcThreads, 2) lin_chunk_kernel(LinArgs A) {
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks)
                         lc_mma_ss(tmem + kLcO, lc_desc(base + SH::V + (uint32_t)ks * 2048u, vlbo),
-                                  lc_desc(base + SH::P + (uint32_t)x * 8192u + (uint32_t)ks * 32u, 16u), id, 1u);
+                                  lc_desc(base + SH::P + (uint32_t)x * 8192u + (uint32_t)ks * 32u, 16u),
+                                  id | (x == 1 ? kLcNegB : 0u), 1u);
                 umma_commit(&bar[0]);
             }
             constexpr uint32_t id = lc_idesc(128, D, 1, 1);  // V^T K'
@@ -399,7 +404,8 @@ __global__ void __launch_bounds__(kLcThreads, 2) lin_chunk_kernel(LinArgs A) {
                 for (int ks = 0; ks < C / 16; ++ks) {
                     const uint32_t kb = x == 0 ? SH::QK + 8192u : SH::KM + (uint32_t)(x - 1) * (KB * 8192u);
                     lc_mma_ss(tmem + kLcR, lc_desc(base + SH::V + (uint32_t)ks * 2048u, vlbo),
-                              lc_desc(base + kb + (uint32_t)ks * 2048u, x == 0 ? 16384u : 8192u), id, x < 2 || ks > 0);
+                              lc_desc(base + kb + (uint32_t)ks * 2048u, x == 0 ? 16384u : 8192u),
+                              id | (x == 1 ? kLcNegB : 0u), x < 2 || ks > 0);
                 }
             umma_commit(&bar[1]);
         }

@@ -21,15 +21,18 @@
 // summed.  The CTA's warps, one of each kind on every scheduler:
 //   0 .. 7   the state: scaled, and cut into the pieces of an A operand in
 //            tensor memory; read from and written to global memory
-//   8 .. 11  the outputs, from tensor memory to global memory
-//   12 .. 15 K' = k / G in three pieces to shared memory
+//   8 .. 15  four for the outputs, from tensor memory to global memory, and
+//            four, with 20, 22 and 23, for K' = k / G, in three pieces to shared
+//            memory
 //   16, 17, 21  the scores Q K^T, a block of 32 x 32 each: from tensor memory,
 //            times 1 / G, masked, in three pieces to shared memory
-//   18       one thread issues every product, in the order Q K^T of chunk c,
-//            V^T P^T of c - 1, V^T K' of c, S^T Q^T of c
+//   18       one thread issues every product, in the order V^T P^T of chunk
+//            c - 1, then Q K^T, V^T K' and S^T Q^T of chunk c
 //   19       the feeder: gates and their products, the chunk's bounds, and the
-//            TMA loads, up to three chunks ahead
-// They meet in mbarriers only.
+//            TMA loads
+// They meet in mbarriers only.  A barrier's waiters look at the parity of a
+// phase, so none may end twice before all have seen it once: where one side can
+// be a chunk ahead, there is a barrier for even and one for odd chunks.
 #pragma once
 
 #include <cuda.h>
@@ -39,7 +42,6 @@
 namespace lq {
 
 constexpr int kLpThreads = 24 * 32;
-constexpr int kLpStages = 3;   // chunks of q, k, v in shared memory
 constexpr int kLpRing = 4;     // chunk descriptions
 constexpr float kLpMinGate = 0x1p-64f;
 // tensor memory: Q K^T | O^T, two | S pieces | S
@@ -57,19 +59,21 @@ struct __align__(16) LpSlot {
 template <int D>
 struct LpShape {
     static constexpr int KB = D / 64;
+    static constexpr int ST = D == 128 ? 3 : 4;  // chunks of q, k, v in shared memory
+    static constexpr int NK = D == 128 ? 1 : 2;  // chunks of K'
     // a stage: KB blocks of 128 rows (64 of Q, 64 of K) x 128 bytes, KB blocks of 64 rows of V
     static constexpr uint32_t V = KB * 16384u, STAGE = KB * 24576u;
-    static constexpr uint32_t P = kLpStages * STAGE, K = P + 3u * 8192u, RING = K + 3u * KB * 8192u;
+    static constexpr uint32_t P = ST * STAGE, K = P + 3u * 8192u, KBUF = 3u * KB * 8192u, RING = K + NK * KBUF;
     static constexpr uint32_t BAR = RING + kLpRing * (uint32_t)sizeof(LpSlot);
     static constexpr uint32_t SMEM = BAR + 256u + 1024u;
-    // state and output warps at work: all, or those whose lanes are < 64
-    static constexpr int SW = D / 16, OW = D / 32;
+    // state warps at work: all, or those whose lanes are < 64
+    static constexpr int SW = D / 16;
 };
 
 struct LpBars {
-    uint64_t full[kLpStages], empty[kLpStages], ring_full[kLpRing], ring_free[kLpRing];
-    uint64_t qk_done, qk_free, p_ready, k_ready, s_ready, y_done, d_done, o_done[2], o_free[2];
-    uint32_t tmem, fail;
+    uint64_t full[4], empty[4], ring_full[kLpRing], ring_free[kLpRing];
+    uint64_t qk_done, p_ready, s_ready, y_done, k_ready[2], d_done[2], o_done[2], o_free[2];
+    uint32_t tmem, chunks;  // chunks: how many there are, once the feeder knows
 };
 static_assert(sizeof(LpBars) <= 256, "barrier space");
 
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     lin_pipe_kernel(const LinArgs A, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv) {
     using SH = LpShape<D>;
-    constexpr int KB = SH::KB, HD = D / 2, C = 64;
+    constexpr int KB = SH::KB, HD = D / 2, C = 64, ST = SH::ST, NK = SH::NK;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     extern __shared__ uint8_t smem_raw[];
@@ -119,26 +123,25 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const uint32_t base = smem_u32(smem);
 
     if (tid == 0) {
-        for (int i = 0; i < kLpStages; ++i) {
+        for (int i = 0; i < ST; ++i) {
             mbar_init(&bars->full[i], 1);
             mbar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < kLpRing; ++i) {
             mbar_init(&bars->ring_full[i], 1);
-            mbar_init(&bars->ring_free[i], SH::SW + SH::OW + 8);  // key, score and issuing warps too
+            mbar_init(&bars->ring_free[i], SH::SW + 14);  // output, key and score warps too
         }
         mbar_init(&bars->qk_done, 1);
-        mbar_init(&bars->qk_free, 3);
         mbar_init(&bars->p_ready, 3);
-        mbar_init(&bars->k_ready, 4);
         mbar_init(&bars->s_ready, SH::SW);
         mbar_init(&bars->y_done, 1);
-        mbar_init(&bars->d_done, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->k_ready[i], 7);
+            mbar_init(&bars->d_done[i], 1);
             mbar_init(&bars->o_done[i], 1);
-            mbar_init(&bars->o_free[i], SH::OW);
+            mbar_init(&bars->o_free[i], 4);
         }
-        bars->fail = 0u;
+        bars->chunks = 0xFFFFFFFFu;
         fence_mbar_init();
     }
     pdl_wait();
@@ -231,8 +234,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 const float ge = __shfl_sync(0xFFFFFFFFu, g0, ((n - 1) >> 1) & 31), go = __shfl_sync(0xFFFFFFFFu, g1, ((n - 1) >> 1) & 31);
                 const float g_last = ((n - 1) & 1) ? go : ge;
 
-                const uint32_t st = c % kLpStages;
-                if (c >= kLpStages) wait(&bars->empty[st], c / kLpStages - 1u);
+                const uint32_t st = c % ST;
+                if (c >= ST) wait(&bars->empty[st], c / ST - 1u);
                 if (ok && lc_elect()) {
                     uint8_t *sp = smem + st * SH::STAGE;
                     mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
@@ -270,90 +273,91 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         if (lane == 0) sl->flags = kLpEnd;
         arrive(&bars->ring_full[r % kLpRing]);
         // what has been asked for lands before the CTA leaves
-        for (uint32_t i = c > kLpStages ? c - kLpStages : 0u; i < c; ++i)
-            mbar_wait_bounded(&bars->full[i % kLpStages], (i / kLpStages) & 1u);
+        for (uint32_t i = c >= ST ? c - ST + 1u : 0u; i < c; ++i) wait(&bars->full[i % ST], i / ST);
+        if (c >= ST) wait(&bars->empty[c % ST], c / ST - 1u);
+        if (lane == 0) bars->chunks = c;
+        arrive(&bars->full[c % ST]);  // the issuer learns the end here
     } else if (warp == 18) {
         // ------------------------------------------------------- the issuer
-        constexpr uint32_t id64 = lc_idesc(128, 64, 0, 0), idpv = lc_idesc(128, 64, 1, 0), idpv2 = lc_idesc(128, 32, 1, 0),
-                           idd = lc_idesc(128, D, 1, 1);
+        constexpr uint32_t id64 = lc_idesc(128, 64, 0, 0), idpv = lc_idesc(128, 64, 1, 0),
+                           idpv2 = lc_idesc(128, 32, 1, 0), idd = lc_idesc(128, D, 1, 1);
         constexpr uint32_t vlbo = KB > 1 ? 8192u : 0u;  // D = 64: lanes 64 .. repeat the others
-        uint32_t c = 0;
-        auto pv = [&](uint32_t i) {  // O^T += V^T P^T of chunk i
-            wait(&bars->p_ready, i);
-            if (ok && lc_elect()) {
-                tc_fence_after();
-                const uint32_t vb = lc_desc(base + (i % kLpStages) * SH::STAGE + SH::V, vlbo), o = tmem + kLpO + 64u * (i & 1u);
-#pragma unroll
-                for (int x = 2; x >= 0; --x) {
-                    const uint32_t pb = lc_desc(base + SH::P, 16u) + (uint32_t)x * 512u;
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)  // tokens 32 .. reach rows 32 .. only
-                        if (ks < 2)
-                            lc_mma_ss(o, vb + ks * 128u, pb + ks * 2u, idpv, 1u);
-                        else
-                            lc_mma_ss(o + 32u, vb + ks * 128u, pb + 256u + ks * 2u, idpv2, 1u);
-                }
-                umma_commit(&bars->o_done[i & 1u]);
-                umma_commit(&bars->empty[i % kLpStages]);
-            }
-            __syncwarp();
-        };
+        // A tcgen05.mma takes its operands' descriptions from uniform registers:
+        // the bases pass through a shuffle, so that the compiler sees them as
+        // such and adds to them there.  This warp gets a sixth of a scheduler's
+        // slots: what it executes per product bounds the kernel.
+        auto uni = [](uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); };
+        const uint32_t pd = uni(lc_desc(base + SH::P, 16u)), td = uni(tmem);
+        const uint32_t q0 = uni(lc_desc(base, 16u)), v0 = uni(lc_desc(base + SH::V, vlbo)), k0 = uni(lc_desc(base + SH::K, 8192u));
+        uint32_t c = 0, st = 0, full_ph = 0, before = 0;  // before: 16-byte units to the stage of chunk c - 1
 #pragma unroll 1
-        for (uint32_t r = 0; ok; ++r) {
-            wait(&bars->ring_full[r % kLpRing], r / kLpRing);
-            const int flags = ok ? ring[r % kLpRing].flags : kLpEnd;
-            arrive(&bars->ring_free[r % kLpRing]);
-            if (flags & kLpEnd) break;
-            if (flags & kLpNone) continue;
-            const uint32_t sb = base + (c % kLpStages) * SH::STAGE;
-            wait(&bars->full[c % kLpStages], c / kLpStages);
-            if (c > 0) wait(&bars->qk_free, c - 1u);
-            if (ok && lc_elect()) {  // Q K^T; rows 64 .. 127 (K K^T) are not used
+        for (; ok; ++c) {
+            wait(&bars->full[st], full_ph);
+            if (c > 0) wait(&bars->p_ready, c - 1u);
+            if (!ok) break;
+            const bool more = c < *reinterpret_cast<volatile uint32_t *>(&bars->chunks);
+            const uint32_t at = uni(st * (SH::STAGE / 16u)), prev = uni(before);
+            const uint32_t o_prev = uni(td + kLpO + 64u * ((c & 1u) ^ 1u)), o = uni(td + kLpO + 64u * (c & 1u));
+            if (lc_elect()) {
                 tc_fence_after();
+                if (c > 0) {  // O^T += V^T P^T of chunk c - 1
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t o = lc_desc(sb, 16u) + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u;
-                    lc_mma_ss(tmem + kLpQK, o, o + 512u, id64, ks > 0);
+                    for (int x = 2; x >= 0; --x)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)  // tokens 32 .. reach rows 32 .. only
+                            lc_mma_ss(ks < 2 ? o_prev : o_prev + 32u, v0 + prev + ks * 128u,
+                                      pd + x * 512u + (ks < 2 ? 0u : 256u) + ks * 2u,
+                                      (ks < 2 ? idpv : idpv2) | (x == 1 ? kLcNegB : 0u), 1u);
+                    umma_commit(&bars->o_done[(c & 1u) ^ 1u]);
+                    umma_commit(&bars->empty[st == 0u ? ST - 1 : st - 1u]);
                 }
-                umma_commit(&bars->qk_done);
+                if (more) {  // Q K^T; rows 64 .. 127 (K K^T) are not used
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t qd = q0 + at + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u;
+                        lc_mma_ss(td + kLpQK, qd, qd + 512u, id64, ks > 0);
+                    }
+                    umma_commit(&bars->qk_done);
+                }
             }
             __syncwarp();
-            if (c > 0) pv(c - 1u);
-            wait(&bars->k_ready, c);
+            if (!more) break;
+            wait(&bars->k_ready[c % NK], c / NK);
             wait(&bars->s_ready, c);
-            if (ok && lc_elect()) {  // S += V^T K'
+            if (c > 1) wait(&bars->o_free[c & 1u], c / 2u - 1u);
+            if (!ok) break;
+            const uint32_t kd = uni(k0 + (c % NK) * (SH::KBUF / 16u));
+            if (lc_elect()) {
                 tc_fence_after();
 #pragma unroll
-                for (int x = 2; x >= 0; --x)
+                for (int x = 2; x >= 0; --x)  // S += V^T K'
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks)
-                        lc_mma_ss(tmem + kLpS, lc_desc(sb + SH::V, vlbo) + ks * 128u,
-                                  lc_desc(base + SH::K, 8192u) + (uint32_t)x * (KB * 512u) + ks * 128u, idd, 1u);
-                umma_commit(&bars->d_done);
-            }
-            __syncwarp();
-            if (c > 1) wait(&bars->o_free[c & 1u], c / 2u - 1u);
-            if (ok && lc_elect()) {  // S^T Q^T
-                tc_fence_after();
+                        lc_mma_ss(td + kLpS, v0 + at + ks * 128u, kd + x * (KB * 512) + ks * 128u, idd | (x == 1 ? kLcNegB : 0u), 1u);
+                umma_commit(&bars->d_done[c % NK]);
 #pragma unroll
-                for (int x = 2; x >= 0; --x)
+                for (int x = 2; x >= 0; --x)  // S^T Q^T
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        lc_mma_ts(tmem + kLpO + 64u * (c & 1u), tmem + kLpSp + (uint32_t)(x * HD + 8 * ks),
-                                  lc_desc(sb, 16u) + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u, id64,
+                        lc_mma_ts(o, td + kLpSp + (uint32_t)(x * HD + 8 * ks),
+                                  q0 + at + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u, id64 | (x == 1 ? kLcNegA : 0u),
                                   x < 2 || ks > 0);
                 umma_commit(&bars->y_done);
             }
             __syncwarp();
-            ++c;
+            before = at;
+            if (++st == (uint32_t)ST) {
+                st = 0;
+                full_ph ^= 1u;
+            }
         }
-        if (c > 0 && ok) pv(c - 1u);
         // every product has ended before tensor memory is given back
         if (c > 0) mbar_wait_bounded(&bars->o_done[(c - 1u) & 1u], ((c - 1u) / 2u) & 1u);
-    } else if (warp >= 12 && warp < 16) {
+    } else if (warp == 20 || warp >= 22 || (warp >= 8 && warp < 16 && (D == 128 ? warp >= 12 : (warp & 3) >= 2))) {
         // ------------------------------------------------- k / G, in pieces
-        constexpr int NP = 8 * KB, NT = 128;
-        const int kt = tid - 384;
+        constexpr int NP = 8 * KB, NT = 7 * 32;
+        const int kw = warp == 20 ? 4 : warp >= 22 ? warp - 17 : D == 128 ? warp - 12 : (warp & 1) + (warp >= 12 ? 2 : 0);
+        const int kt = 32 * kw + lane;
         uint32_t c = 0;
 #pragma unroll 1
         for (uint32_t r = 0; ok; ++r) {
@@ -366,9 +370,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 continue;
             }
             const int n = sl->n;
-            uint8_t *sp = smem + (c % kLpStages) * SH::STAGE;
-            wait(&bars->full[c % kLpStages], c / kLpStages);
-            if (c > 0) wait(&bars->d_done, c - 1u);
+            uint8_t *sp = smem + (c % ST) * SH::STAGE;
+            wait(&bars->full[c % ST], c / ST);
+            if (c >= NK) wait(&bars->d_done[c % NK], c / NK - 1u);
             if (ok) {
 #pragma unroll 2
                 for (int x = kt; x < C * NP; x += NT) {
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                         const float2 kf = __fmul2_rn(f, make_float2(__uint_as_float(u[z] << 16), __uint_as_float(u[z] & 0xFFFF0000u)));
                         lc_split2(kf.x, kf.y, hi[z], mid[z], lo[z]);
                     }
-                    uint8_t *dp = smem + SH::K + tile_off(t, pc, 8192u);
+                    uint8_t *dp = smem + SH::K + (c % NK) * SH::KBUF + tile_off(t, pc, 8192u);
                     *reinterpret_cast<uint4 *>(dp) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(dp + KB * 8192) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
                     *reinterpret_cast<uint4 *>(dp + 2 * KB * 8192) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     *reinterpret_cast<uint4 *>(sp + SH::V + tile_off(n + x / NP, x % NP, 8192u)) = make_uint4(0u, 0u, 0u, 0u);
                 fence_async_smem();
             }
-            arrive(&bars->k_ready);
+            arrive(&bars->k_ready[c % NK]);
             arrive(&bars->ring_free[r % kLpRing]);
             ++c;
         }
@@ -419,9 +423,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             tmem_ld16_async(tlane + kLpQK + (uint32_t)c0 + 16u, v[1]);
             tmem_ld_wait(v[0]);
             tmem_ld_wait(v[1]);
-            tc_fence_before();
-            arrive(&bars->qk_free);
-            if (c > 0) wait(&bars->o_done[(c - 1u) & 1u], (c - 1u) / 2u);
+            // (V^T P^T of the chunk before was issued before Q K^T: P is free)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -443,62 +445,66 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     *reinterpret_cast<uint4 *>(o + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             fence_async_smem();
+            tc_fence_before();
             arrive(&bars->p_ready);
             arrive(&bars->ring_free[r % kLpRing]);
             ++c;
         }
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp >= 8 && warp < 16) {
         // ------------------------------------------------------ the outputs
-        if ((warp & 3) < D / 32) {
-            const int j = 32 * (warp & 3) + lane;
-            constexpr int NT = SH::OW * 32;
-            const uint32_t step = (uint32_t)A.map.heads * D;  // < 2^31
-            uint32_t c = 0;
+        // D = 128: 64 tokens of 32 value channels each; D = 64: 32 tokens
+        const int j = 32 * (warp & 3) + lane;
+        constexpr int TN = D / 2, NT = 128;
+        const int x0 = D == 64 && warp >= 12 ? 32 : 0;
+        const int ot = 32 * (D == 128 ? warp - 8 : (warp & 1) + (warp >= 12 ? 2 : 0)) + lane;
+        const uint32_t step = (uint32_t)A.map.heads * D;  // < 2^31
+        uint32_t c = 0;
 #pragma unroll 1
-            for (uint32_t r = 0; ok; ++r) {
-                wait(&bars->ring_full[r % kLpRing], r / kLpRing);
-                const LpSlot *sl = ring + r % kLpRing;
-                const int flags = ok ? sl->flags : kLpEnd;
-                if (flags & kLpEnd) {
-                    arrive(&bars->ring_free[r % kLpRing]);
-                    break;
-                }
-                const int row = sl->w / A.map.heads, hh = sl->w - row * A.map.heads, n = sl->n;
-                if (!(flags & kLpNone)) {
-                    float *o = A.out + lin_v_row(A, row, hh, sl->t0) * D + j;
-                    wait(&bars->o_done[c & 1u], c / 2u);
-                    tc_fence_after();
+        for (uint32_t r = 0; ok; ++r) {
+            wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            const LpSlot *sl = ring + r % kLpRing;
+            const int flags = ok ? sl->flags : kLpEnd;
+            if (flags & kLpEnd) break;
+            const int row = sl->w / A.map.heads, hh = sl->w - row * A.map.heads, n = sl->n;
+            if (!(flags & kLpNone)) {
+                float *o = A.out + lin_v_row(A, row, hh, sl->t0 + x0) * D + j;
+                wait(&bars->o_done[c & 1u], c / 2u);
+                tc_fence_after();
 #pragma unroll 1
-                    for (int x = 0; x < C; x += 32) {
-                        uint32_t v[2][16];
-                        tmem_ld16_async(tlane + kLpO + 64u * (c & 1u) + (uint32_t)x, v[0]);
-                        tmem_ld16_async(tlane + kLpO + 64u * (c & 1u) + (uint32_t)x + 16u, v[1]);
-                        tmem_ld_wait(v[0]);
-                        tmem_ld_wait(v[1]);
-                        if (x + 32 >= C) {
-                            tc_fence_before();
-                            arrive(&bars->o_free[c & 1u]);
-                        }
-                        if (A.out && ok)
-#pragma unroll
-                            for (int y = 0; y < 32; y += 4) {
-                                const float4 g = *reinterpret_cast<const float4 *>(sl->G + x + y);
-                                const float gg[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    if (x + y + z < n)
-                                        o[(uint64_t)(uint32_t)(y + z) * step] = __uint_as_float(v[(y + z) >> 4][(y + z) & 15]) * gg[z];
-                            }
-                        o += (size_t)32 * step;
+                for (int x = x0; x < x0 + TN; x += 32) {
+                    uint32_t v[2][16];
+                    tmem_ld16_async(tlane + kLpO + 64u * (c & 1u) + (uint32_t)x, v[0]);
+                    tmem_ld16_async(tlane + kLpO + 64u * (c & 1u) + (uint32_t)x + 16u, v[1]);
+                    tmem_ld_wait(v[0]);
+                    tmem_ld_wait(v[1]);
+                    if (x + 32 >= x0 + TN) {
+                        tc_fence_before();
+                        arrive(&bars->o_free[c & 1u]);
                     }
-                    ++c;
+                    auto put = [&](int left) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4) {
+                            const float4 g = *reinterpret_cast<const float4 *>(sl->G + x + y);
+                            const float gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                if (y + z < left)
+                                    o[(uint64_t)(uint32_t)(y + z) * step] = __uint_as_float(v[(y + z) >> 4][(y + z) & 15]) * gg[z];
+                        }
+                    };
+                    if (A.out && ok) {
+                        if (n == C) put(32);
+                        else put(n - x);
+                    }
+                    o += (size_t)32 * step;
                 }
-                if ((flags & kLpLast) && A.out && ok)  // no outputs past the prompt's end
-                    for (int x = tid - 256; x < (sl->zero_end - sl->t0 - n) * (D / 4); x += NT)
-                        *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, sl->t0 + n + x / (D / 4)) * D +
-                                                    4 * (x % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
-                arrive(&bars->ring_free[r % kLpRing]);
+                ++c;
             }
+            if ((flags & kLpLast) && A.out && ok)  // no outputs past the prompt's end
+                for (int x = ot; x < (sl->zero_end - sl->t0 - n) * (D / 4); x += NT)
+                    *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, sl->t0 + n + x / (D / 4)) * D + 4 * (x % (D / 4))) =
+                        make_float4(0.f, 0.f, 0.f, 0.f);
+            arrive(&bars->ring_free[r % kLpRing]);
         }
     } else if (warp < 8 && (warp & 3) < D / 32) {
         // -------------------------------------------------------- the state
@@ -517,7 +523,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 break;
             }
             w = sl->w;
-            if (c > 0) wait(&bars->d_done, c - 1u);
+            // S^T Q^T of the chunk before, and with it V^T K', which was issued before it
+            if (c > 0) wait(&bars->y_done, c - 1u);
             tc_fence_after();
             if (flags & kLpFirst) {
                 const int bi = A.map.blob(w);
@@ -547,8 +554,6 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             }
             if (!(flags & kLpNone)) {
                 // ---- S scaled, and S^T in three pieces (pairs of key channels)
-                if (c > 0) wait(&bars->y_done, c - 1u);
-                tc_fence_after();
 #pragma unroll 1
                 for (int x = 0; x < HD; x += 32) {
                     uint32_t v[2][16];
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 ++c;
             }
             if ((flags & kLpFinal) && ok) {  // the prompt's end
-                if (!(flags & kLpNone)) wait(&bars->d_done, c - 1u);
+                if (!(flags & kLpNone)) wait(&bars->y_done, c - 1u);
                 tc_fence_after();
                 uint8_t *blob = A.state + (size_t)A.map.blob(w) * A.L.blob;
                 float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + (size_t)(HD * half) * D + j;
