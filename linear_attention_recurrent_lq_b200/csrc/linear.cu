@@ -7,8 +7,8 @@
 #include "lq_common.cuh"
 #include "lq_host.cuh"
 #include "lq_linear.cuh"
-#include "lq_linear_chunked.cuh"
 #include "lq_linear_pipe.cuh"
+#include "lq_linear_state.cuh"
 #include "lq_norms.cuh"
 
 using namespace lq;
@@ -54,26 +54,6 @@ lq_status check_linear(const lq_config *cfg, int qk_heads) {
     return LQ_OK;
 }
 
-template <typename... KArgs>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster, uint32_t smem, cudaStream_t s,
-                           LinArgs a) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
 template <int D, bool BF16>
 lq_status launch_step(const LinArgs &a, cudaStream_t s) {
     // few heads: four CTAs per head, so that every SM has loads in flight
@@ -109,15 +89,15 @@ lq_status launch_recurrent(const LinArgs &a, cudaStream_t s) {
     if (a.nseg > 1) {
         auto k = lin_recurrent_kernel<D, BF16, C, true>;
         if (allow_smem(k, SH::SMEM) != cudaSuccess) return LQ_ERR_CUDA;
-        if (launch_cluster(k, dim3((unsigned)(a.work * SH::NB), (unsigned)(a.nseg - 1)), kLinThreads, 1, SH::SMEM, s,
-                           a) != cudaSuccess)
+        if (launch_pdl(k, dim3((unsigned)(a.work * SH::NB), (unsigned)(a.nseg - 1)), kLinThreads, 1, SH::SMEM, s,
+                       a) != cudaSuccess)
             return LQ_ERR_CUDA;
         if (launch_pdl(lin_scan_kernel<D>, a.work * (D * D / 1024), 256, 0u, s, a) != cudaSuccess) return LQ_ERR_CUDA;
     }
     auto k = lin_recurrent_kernel<D, BF16, C, false>;
     if (allow_smem(k, SH::SMEM) != cudaSuccess) return LQ_ERR_CUDA;
-    return launched(launch_cluster(k, dim3((unsigned)(a.work * SH::NB), (unsigned)a.nseg), kLinThreads, SH::NB,
-                                   SH::SMEM, s, a));
+    return launched(launch_pdl(k, dim3((unsigned)(a.work * SH::NB), (unsigned)a.nseg), kLinThreads, SH::NB,
+                               SH::SMEM, s, a));
 }
 
 // A [rows, cols] bf16 tensor as boxes of 64 rows x 64 columns, 128-byte swizzle.
@@ -143,19 +123,19 @@ bool make_map(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows) {
 
 template <int D>
 lq_status launch_chunked(const LinArgs &a, cudaStream_t s) {
-    if (a.nseg > 1) {
-        const uint32_t smem = LcShape<D>::SMEM;
-        auto k = lin_chunk_kernel<D, true>;
-        if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;
-        if (launch_cluster(k, dim3((unsigned)a.work, (unsigned)(a.nseg - 1)), kLcThreads, 1, smem, s, a) != cudaSuccess)
-            return LQ_ERR_CUDA;
-        if (launch_pdl(lin_scan_kernel<D>, a.work * (D * D / 1024), 256, 0u, s, a) != cudaSuccess) return LQ_ERR_CUDA;
-    }
     CUtensorMap mq, mk, mv;
     const uint64_t rows = (uint64_t)(a.work / a.map.heads) * a.tokens;
     if (!make_map(&mq, a.q, (uint64_t)a.qk_heads * D, rows) || !make_map(&mk, a.k, (uint64_t)a.qk_heads * D, rows) ||
         !make_map(&mv, a.v, (uint64_t)a.map.heads * D, rows))
         return LQ_ERR_CUDA;
+    if (a.nseg > 1) {
+        const uint32_t smem = LsShape<D>::SMEM;
+        auto k = lin_state_kernel<D>;
+        if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;
+        if (launch_pdl(k, dim3((unsigned)a.work, (unsigned)(a.nseg - 1)), kLsThreads, 1, smem, s, a, mk, mv) != cudaSuccess)
+            return LQ_ERR_CUDA;
+        if (launch_pdl(lin_scan_kernel<D>, a.work * (D * D / 1024), 256, 0u, s, a) != cudaSuccess) return LQ_ERR_CUDA;
+    }
     const uint32_t smem = LpShape<D>::SMEM;
     auto k = lin_pipe_kernel<D>;
     if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;

@@ -62,21 +62,31 @@ cudaError_t allow_smem(K kernel, uint32_t bytes) {
 
 // Launch with programmatic stream serialization: the kernel may start while
 // the previous kernel on the stream drains; it waits for that kernel's
-// completion (pdl_wait) before its first global-memory access.
+// completion (pdl_wait) before its first global-memory access.  `cluster`:
+// CTAs of a thread-block cluster along x.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), int grid, int threads, uint32_t smem, cudaStream_t s,
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster, uint32_t smem, cudaStream_t s,
                        Args &&...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), int grid, int threads, uint32_t smem, cudaStream_t s, Args &&...args) {
+    return launch_pdl(kernel, dim3((unsigned)grid), threads, 1, smem, s, std::forward<Args>(args)...);
 }
 
 inline lq_status launched(cudaError_t e) {

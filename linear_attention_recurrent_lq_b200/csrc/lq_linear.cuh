@@ -9,7 +9,7 @@
 // Kernels here: one token (lin_step_kernel), a prompt token after token
 // (lin_recurrent_kernel, also the first pass of a prompt cut along time), and
 // the pass that joins the cuts (lin_scan_kernel).  The chunkwise form on the
-// tensor cores is in lq_linear_chunked.cuh.  Grouped queries and keys: value
+// tensor cores is in lq_linear_pipe.cuh and lq_linear_state.cuh.  Grouped queries and keys: value
 // head h reads query / key head h / (H / Hk).
 #pragma once
 
@@ -62,6 +62,14 @@ __device__ __forceinline__ int lin_length(const LinArgs &A, int row) {
 // The segment that holds a prompt's last token (0 for an empty prompt).
 __device__ __forceinline__ int lin_last_segment(const LinArgs &A, int len) {
     return len > 0 ? (len - 1) / A.seg_len : 0;
+}
+
+// Where work item w's segment starts from; null: a zero state.
+__device__ __forceinline__ const float *lin_state_source(const LinArgs &A, int w, int seg, const uint8_t *blob) {
+    const size_t n = A.L.pairs_off - A.L.qs_off;  // bytes of a state
+    if (A.nseg > 1) return A.ws_S + ((size_t)w * A.nseg + seg) * (n / 4);
+    if (A.cont) return reinterpret_cast<const float *>(blob + kHdrBytes);
+    return A.S0 ? A.S0 + (size_t)w * (n / 4) : nullptr;
 }
 
 // Header of a blob whose prompt has been taken in.
@@ -232,11 +240,7 @@ __global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
     float2 S[2 * M][C];
     {
         const float *src = nullptr;
-        if (!PARTIAL && run && seg <= last) {
-            if (A.nseg > 1) src = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D);
-            else if (A.cont) src = reinterpret_cast<const float *>(blob + kHdrBytes);
-            else if (A.S0) src = A.S0 + (size_t)w * (D * D);
-        }
+        if (!PARTIAL && run && seg <= last) src = lin_state_source(A, w, seg, blob);
 #pragma unroll
         for (int p = 0; p < 2 * M; ++p)
 #pragma unroll

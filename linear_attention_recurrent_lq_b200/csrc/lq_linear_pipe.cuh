@@ -11,10 +11,6 @@
 // before a token that would take G below 2^-64: 1 / G stays far inside FP32,
 // and a gate of 0 starts a chunk, where it clears the state exactly.
 //
-// Precision: q, k and v are bf16 as they come; every FP32 operand (the state,
-// the scores, k / G) is cut into three bf16 pieces that hold its 24 bits
-// exactly, multiplied smallest first, and summed in FP32.
-//
 // One CTA per SM walks the work items (a head, or a segment of a prompt cut
 // along time) b, b + grid, ... as one stream of chunks.  The state is an FP32
 // accumulator in tensor memory (lane = value channel) onto which V^T K' is
@@ -35,9 +31,7 @@
 // be a chunk ahead, there is a barrier for even and one for odd chunks.
 #pragma once
 
-#include <cuda.h>
-
-#include "lq_linear_chunked.cuh"
+#include "lq_linear_mma.cuh"
 
 namespace lq {
 
@@ -74,39 +68,9 @@ struct LpBars {
     uint64_t full[4], empty[4], ring_full[kLpRing], ring_free[kLpRing];
     uint64_t qk_done, p_ready, s_ready, y_done, k_ready[2], d_done[2], o_done[2], o_free[2];
     uint32_t tmem, chunks;  // chunks: how many there are, once the feeder knows
+    uint32_t from_zero[4];  // per stage: the chunk starts from a zero state
 };
 static_assert(sizeof(LpBars) <= 256, "barrier space");
-
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// 16 columns, without the wait (tmem_ld_wait before the first use)
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-// Wait for the loads above; the registers pass through, so that no use is
-// scheduled before it.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 ::"memory");
-}
-
-__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
 
 template <int D>
 __global__ void __launch_bounds__(kLpThreads, 1)
@@ -163,9 +127,6 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(b);
     };
-    auto tile_off = [&](int r, int c, uint32_t block) -> uint32_t {  // row r, 16-byte piece c
-        return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-    };
 
     if (warp == 19) {
         // ------------------------------------------------------- the feeder
@@ -208,6 +169,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 ++r;
                 continue;
             }
+            const float *src = lin_state_source(A, w, seg, blob);
+            const bool from_zero = src == nullptr;
+            // the state warps read it some chunks from now
+            if (src && lane == 0) bulk_prefetch_l2(src, D * D * 4);
             const int xq = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens;
 #pragma unroll 1
             for (int t0 = t_begin; t0 < t_stop && ok;) {
@@ -238,6 +203,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 if (c >= ST) wait(&bars->empty[st], c / ST - 1u);
                 if (ok && lc_elect()) {
                     uint8_t *sp = smem + st * SH::STAGE;
+                    bars->from_zero[st] = from_zero && t0 == t_begin;
                     mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
@@ -289,7 +255,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         auto uni = [](uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); };
         const uint32_t pd = uni(lc_desc(base + SH::P, 16u)), td = uni(tmem);
         const uint32_t q0 = uni(lc_desc(base, 16u)), v0 = uni(lc_desc(base + SH::V, vlbo)), k0 = uni(lc_desc(base + SH::K, 8192u));
-        uint32_t c = 0, st = 0, full_ph = 0, before = 0;  // before: 16-byte units to the stage of chunk c - 1
+        uint32_t c = 0, st = 0, full_ph = 0, acc = 1, before = 0;  // before: 16-byte units to the stage of chunk c - 1
 #pragma unroll 1
         for (; ok; ++c) {
             wait(&bars->full[st], full_ph);
@@ -297,6 +263,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             if (!ok) break;
             const bool more = c < *reinterpret_cast<volatile uint32_t *>(&bars->chunks);
             const uint32_t at = uni(st * (SH::STAGE / 16u)), prev = uni(before);
+            const uint32_t acc_prev = uni(acc);  // whether O^T of chunk c - 1 holds S^T Q^T
             const uint32_t o_prev = uni(td + kLpO + 64u * ((c & 1u) ^ 1u)), o = uni(td + kLpO + 64u * (c & 1u));
             if (lc_elect()) {
                 tc_fence_after();
@@ -307,7 +274,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                         for (int ks = 0; ks < 4; ++ks)  // tokens 32 .. reach rows 32 .. only
                             lc_mma_ss(ks < 2 ? o_prev : o_prev + 32u, v0 + prev + ks * 128u,
                                       pd + x * 512u + (ks < 2 ? 0u : 256u) + ks * 2u,
-                                      (ks < 2 ? idpv : idpv2) | (x == 1 ? kLcNegB : 0u), 1u);
+                                      (ks < 2 ? idpv : idpv2) | (x == 1 ? kLcNegB : 0u), x < 2 || ks > 0 ? 1u : acc_prev);
                     umma_commit(&bars->o_done[(c & 1u) ^ 1u]);
                     umma_commit(&bars->empty[st == 0u ? ST - 1 : st - 1u]);
                 }
@@ -324,24 +291,27 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             if (!more) break;
             wait(&bars->k_ready[c % NK], c / NK);
             wait(&bars->s_ready, c);
-            if (c > 1) wait(&bars->o_free[c & 1u], c / 2u - 1u);
             if (!ok) break;
             const uint32_t kd = uni(k0 + (c % NK) * (SH::KBUF / 16u));
+            acc = uni(*reinterpret_cast<volatile uint32_t *>(&bars->from_zero[st])) ? 0u : 1u;
             if (lc_elect()) {
                 tc_fence_after();
 #pragma unroll
                 for (int x = 2; x >= 0; --x)  // S += V^T K'
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks)
-                        lc_mma_ss(td + kLpS, v0 + at + ks * 128u, kd + x * (KB * 512) + ks * 128u, idd | (x == 1 ? kLcNegB : 0u), 1u);
+                        lc_mma_ss(td + kLpS, v0 + at + ks * 128u, kd + x * (KB * 512) + ks * 128u, idd | (x == 1 ? kLcNegB : 0u),
+                                  x < 2 || ks > 0 ? 1u : acc);
                 umma_commit(&bars->d_done[c % NK]);
+                if (acc) {  // S^T Q^T
 #pragma unroll
-                for (int x = 2; x >= 0; --x)  // S^T Q^T
+                    for (int x = 2; x >= 0; --x)
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        lc_mma_ts(o, td + kLpSp + (uint32_t)(x * HD + 8 * ks),
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            lc_mma_ts(o, td + kLpSp + (uint32_t)(x * HD + 8 * ks),
                                   q0 + at + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u, id64 | (x == 1 ? kLcNegA : 0u),
                                   x < 2 || ks > 0);
+                }
                 umma_commit(&bars->y_done);
             }
             __syncwarp();
@@ -378,23 +348,12 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 for (int x = kt; x < C * NP; x += NT) {
                     const int t = x / NP, pc = x % NP;
                     uint4 kk = make_uint4(0u, 0u, 0u, 0u);  // rows behind the chunk
-                    if (t < n) kk = *reinterpret_cast<const uint4 *>(sp + 8192 + tile_off(t, pc, 16384u));
-                    const uint32_t u[4] = {kk.x, kk.y, kk.z, kk.w};
-                    const float2 f = make_float2(sl->inv[t], sl->inv[t]);
-                    uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float2 kf = __fmul2_rn(f, make_float2(__uint_as_float(u[z] << 16), __uint_as_float(u[z] & 0xFFFF0000u)));
-                        lc_split2(kf.x, kf.y, hi[z], mid[z], lo[z]);
-                    }
-                    uint8_t *dp = smem + SH::K + (c % NK) * SH::KBUF + tile_off(t, pc, 8192u);
-                    *reinterpret_cast<uint4 *>(dp) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(dp + KB * 8192) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    *reinterpret_cast<uint4 *>(dp + 2 * KB * 8192) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (t < n) kk = *reinterpret_cast<const uint4 *>(sp + 8192 + lc_tile_off(t, pc, 16384u));
+                    lc_weighted_piece(kk, sl->inv[t], smem + SH::K + (c % NK) * SH::KBUF + lc_tile_off(t, pc, 8192u), KB * 8192u);
                 }
                 // rows of V behind the chunk meet zeros of P and K', so they must be finite
                 for (int x = kt; x < (C - n) * NP; x += NT)
-                    *reinterpret_cast<uint4 *>(sp + SH::V + tile_off(n + x / NP, x % NP, 8192u)) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(sp + SH::V + lc_tile_off(n + x / NP, x % NP, 8192u)) = make_uint4(0u, 0u, 0u, 0u);
                 fence_async_smem();
             }
             arrive(&bars->k_ready[c % NK]);
@@ -439,7 +398,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                                                      make_float2(f[2 * z], f[2 * z + 1]));
                         lc_split2(s0 + 2 * z <= diag ? x2.x : 0.f, s0 + 2 * z + 1 <= diag ? x2.y : 0.f, hi[z], mid[z], lo[z]);
                     }
-                    uint8_t *o = smem + SH::P + tile_off(t, (c0 + s0) >> 3, 0u);
+                    uint8_t *o = smem + SH::P + lc_tile_off(t, (c0 + s0) >> 3, 0u);
                     *reinterpret_cast<uint4 *>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(o + 8192) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
                     *reinterpret_cast<uint4 *>(o + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -512,6 +471,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const uint32_t ts = tlane + kLpS + (uint32_t)(HD * half), tp = tlane + kLpSp + (uint32_t)(HD / 2 * half);
         uint32_t c = 0;
         float g = 1.f;  // scale of the accumulator
+        bool from_zero = false;
         int w = 0;
 #pragma unroll 1
         for (uint32_t r = 0; ok; ++r) {
@@ -525,18 +485,16 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             w = sl->w;
             // S^T Q^T of the chunk before, and with it V^T K', which was issued before it
             if (c > 0) wait(&bars->y_done, c - 1u);
+            if (c > 1) wait(&bars->o_free[c & 1u], c / 2u - 1u);  // for S^T Q^T of this chunk
             tc_fence_after();
             if (flags & kLpFirst) {
                 const int bi = A.map.blob(w);
                 const float *src = nullptr;
-                if (!(flags & kLpNone) || (flags & kLpFinal)) {
-                    if (A.nseg > 1) src = A.ws_S + ((size_t)w * A.nseg + sl->seg) * (D * D);
-                    else if (A.cont) src = reinterpret_cast<const float *>(A.state + (size_t)bi * A.L.blob + kHdrBytes);
-                    else if (A.S0) src = A.S0 + (size_t)w * (D * D);
-                }
+                if (!(flags & kLpNone) || (flags & kLpFinal)) src = lin_state_source(A, w, sl->seg, A.state + (size_t)bi * A.L.blob);
+                from_zero = src == nullptr && !(flags & kLpNone);
                 if (src) src += (size_t)(HD * half) * D + j;
 #pragma unroll 1
-                for (int x = 0; x < HD; x += 32) {
+                for (int x = 0; x < HD && !from_zero; x += 32) {
                     uint32_t v[32];
 #pragma unroll
                     for (int y = 0; y < 32; ++y) v[y] = src ? __float_as_uint(src[(size_t)(x + y) * D]) : 0u;
@@ -553,9 +511,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 g = (flags & kLpNone) ? 1.f : sl->a_first;
             }
             if (!(flags & kLpNone)) {
-                // ---- S scaled, and S^T in three pieces (pairs of key channels)
+                // ---- S scaled, and S^T in three pieces (pairs of key channels); from a
+                // zero state nothing is to be done: the products overwrite
 #pragma unroll 1
-                for (int x = 0; x < HD; x += 32) {
+                for (int x = 0; x < HD && !from_zero; x += 32) {
                     uint32_t v[2][16];
                     tmem_ld16_async(ts + (uint32_t)x, v[0]);
                     tmem_ld16_async(ts + (uint32_t)x + 16u, v[1]);
@@ -580,6 +539,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 arrive(&bars->s_ready);
+                from_zero = false;
                 g = sl->g_next;
                 ++c;
             }

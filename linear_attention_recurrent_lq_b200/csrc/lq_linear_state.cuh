@@ -1,0 +1,184 @@
+// lq_linear_state.cuh -- what a segment of a prompt leaves behind, on the tensor
+// cores: the first pass over a prompt that is cut along time (bf16 k, v;
+// sm_100a: TMA, tcgen05, tensor memory).
+//
+// From a zero state, a segment of tokens t0 .. t1 ends with
+//     S = sum_s W_s k_s v_s^T,   W_s = prod_{s < u <= t1} a_u,
+// one long product: the weights refer to the segment's end, so the accumulator
+// in tensor memory is never scaled.  The chunks of 64 tokens are taken from the
+// last to the first, with the product of the gates behind them carried along
+// (a gate of 0 is exact).  W k is cut into three bf16 pieces.
+//
+// One CTA takes one (head, segment): eight warps weight the keys, one thread
+// issues the products, one warp feeds (gates, TMA).  Bound by HBM: 516 bytes
+// per token and head (d = 128), 1390 clocks per chunk and SM; 768 are tensor
+// time.
+#pragma once
+
+#include "lq_linear_mma.cuh"
+
+namespace lq {
+
+constexpr int kLsThreads = 10 * 32;
+constexpr int kLsStages = 3;
+
+template <int D>
+struct LsShape {
+    static constexpr int KB = D / 64;
+    // a stage: K and V, KB blocks of 64 rows x 128 bytes each
+    static constexpr uint32_t V = KB * 8192u, STAGE = 2u * V, K = kLsStages * STAGE, KBUF = 3u * KB * 8192u;
+    static constexpr uint32_t W = K + 2u * KBUF, BAR = W + kLsStages * 256u, SMEM = BAR + 128u + 1024u;
+};
+
+struct LsBars {
+    uint64_t full[kLsStages], empty[kLsStages], k_ready[2], d_done[2];
+    uint32_t tmem;
+};
+static_assert(sizeof(LsBars) <= 128, "barrier space");
+
+template <int D>
+__global__ void __launch_bounds__(kLsThreads, 1)
+    lin_state_kernel(const LinArgs A, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using SH = LsShape<D>;
+    constexpr int KB = SH::KB, C = 64;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int w = blockIdx.x, seg = blockIdx.y;
+    const int row = w / A.map.heads, hh = w - row * A.map.heads;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    LsBars *bars = reinterpret_cast<LsBars *>(smem + SH::BAR);
+    const uint32_t base = smem_u32(smem);
+    if (tid == 0) {
+        for (int i = 0; i < kLsStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->k_ready[i], 8);
+            mbar_init(&bars->d_done[i], 1);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    // a segment before the one that holds the prompt's end is whole
+    if (A.map.blob(w) < 0 || seg >= lin_last_segment(A, lin_length(A, row))) return;  // uniform: not needed
+    if (warp == 8) tmem_alloc(&bars->tmem, 128u);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    const int t_begin = seg * A.seg_len, chunks = A.seg_len / C;
+    bool ok = true;
+    auto wait = [&](uint64_t *b, uint32_t phase) {
+        if (!mbar_try_wait(b, phase & 1u) && !mbar_wait_bounded(b, phase & 1u)) ok = false;
+    };
+
+    if (warp == 9) {  // the feeder
+        const float *gates = A.decay + lin_v_row(A, row, hh, t_begin);
+        const size_t gs = (size_t)A.map.heads;
+        const int x = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens + t_begin;
+        float carry = 1.f;  // product of the gates behind the chunk
+        int bad = kNoBad;
+        auto gate = [&](int t) -> float { return t >= 0 ? __ldcg(gates + (size_t)t * gs) : 1.f; };
+        float a0 = gate((chunks - 1) * C + 2 * lane), a1 = gate((chunks - 1) * C + 2 * lane + 1);
+#pragma unroll 1
+        for (int i = 0; i < chunks && ok; ++i) {
+            const int at = (chunks - 1 - i) * C;
+            const uint32_t st = (uint32_t)i % kLsStages;
+            if (i >= kLsStages) wait(&bars->empty[st], (uint32_t)i / kLsStages - 1u);
+            const float n0 = gate(at - C + 2 * lane), n1 = gate(at - C + 2 * lane + 1);
+            const unsigned w0 = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(a0));
+            const unsigned w1 = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(a1));
+            if (w0 | w1) bad = t_begin + at + min(w0 ? 2 * (__ffs(w0) - 1) : C, w1 ? 2 * (__ffs(w1) - 1) + 1 : C);
+            float suf = a0 * a1;  // products of the gates from token 2 lane on
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const float y = __shfl_down_sync(0xFFFFFFFFu, suf, d);
+                if (lane + d < 32) suf *= y;
+            }
+            const float after = __shfl_down_sync(0xFFFFFFFFu, suf, 1);
+            const float b1 = (lane < 31 ? after : 1.f) * carry;
+            *reinterpret_cast<float2 *>(smem + SH::W + st * 256u + 8u * lane) = make_float2(a1 * b1, b1);
+            carry *= __shfl_sync(0xFFFFFFFFu, suf, 0);
+            __syncwarp();
+            if (lane == 0 && ok) {
+                uint8_t *sp = smem + st * SH::STAGE;
+                mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    tma_load_2d(sp + kb * 8192, &mk, x + 64 * kb, y0 + at, &bars->full[st]);
+                    tma_load_2d(sp + SH::V + kb * 8192, &mv, xv + 64 * kb, y0 + at, &bars->full[st]);
+                }
+            }
+            a0 = n0;
+            a1 = n1;
+        }
+        if (lane == 0) {
+            A.ws_g[(size_t)w * A.nseg + seg] = carry;
+            A.ws_bad[(size_t)w * A.nseg + seg] = bad;
+        }
+    } else if (warp == 8) {  // the issuer: S^T += V^T K'
+        auto uni = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+        constexpr uint32_t id = lc_idesc(128, D, 1, 1), vlbo = KB > 1 ? 8192u : 0u;
+        const uint32_t v0 = uni(lc_desc(base + SH::V, vlbo)), k0 = uni(lc_desc(base + SH::K, 8192u)), td = uni(tmem);
+#pragma unroll 1
+        for (int i = 0; i < chunks && ok; ++i) {
+            wait(&bars->k_ready[i & 1], (uint32_t)i / 2u);  // the chunk's loads have landed, too
+            const uint32_t vd = uni(v0 + (uint32_t)(i % kLsStages) * (SH::STAGE / 16u)), kd = uni(k0 + (uint32_t)(i & 1) * (SH::KBUF / 16u));
+            const uint32_t acc = uni(i > 0 ? 1u : 0u);
+            if (ok && lc_elect()) {
+                tc_fence_after();
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks)
+                        lc_mma_ss(td, vd + ks * 128u, kd + x * (KB * 512) + ks * 128u, id | (x == 1 ? kLcNegB : 0u),
+                                  x < 2 || ks > 0 ? 1u : acc);
+                umma_commit(&bars->d_done[i & 1]);
+                umma_commit(&bars->empty[i % kLsStages]);
+            }
+            __syncwarp();
+        }
+    } else {  // the keys, then the state to the workspace
+        constexpr int NP = 8 * KB;
+#pragma unroll 1
+        for (int i = 0; i < chunks && ok; ++i) {
+            const uint32_t st = (uint32_t)i % kLsStages;
+            wait(&bars->full[st], (uint32_t)i / kLsStages);
+            if (i >= 2) wait(&bars->d_done[i & 1], (uint32_t)i / 2u - 1u);
+            const float *W = reinterpret_cast<const float *>(smem + SH::W + st * 256u);
+#pragma unroll 2
+            for (int x = tid; x < C * NP; x += 256) {
+                const int t = x / NP, pc = x % NP;
+                const uint32_t o = lc_tile_off(t, pc, 8192u);
+                lc_weighted_piece(*reinterpret_cast<const uint4 *>(smem + st * SH::STAGE + o), W[t],
+                                  smem + SH::K + (i & 1) * SH::KBUF + o, KB * 8192u);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->k_ready[i & 1]);
+        }
+        wait(&bars->d_done[(chunks - 1) & 1], (uint32_t)(chunks - 1) / 2u);
+        tc_fence_after();
+        const int j = 32 * (warp & 3) + lane, half = warp >> 2;
+        if ((warp & 3) < D / 32) {
+            float *dst = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D) + (size_t)(D / 2 * half) * D + j;
+#pragma unroll 1
+            for (int x = 0; x < D / 2; x += 16) {
+                uint32_t v[16];
+                tmem_ld16_async(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(D / 2 * half + x), v);
+                tmem_ld_wait(v);
+#pragma unroll
+                for (int y = 0; y < 16; ++y) dst[(size_t)(x + y) * D] = __uint_as_float(v[y]);
+            }
+        }
+        if (!ok && lane == 0) set_status(A.state + (size_t)A.map.blob(w) * A.L.blob, LQ_DEV_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 128u);
+}
+
+}  // namespace lq
