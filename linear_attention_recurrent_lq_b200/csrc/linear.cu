@@ -139,9 +139,7 @@ lq_status launch_chunked(const LinArgs &a, cudaStream_t s) {
     const uint32_t smem = LpShape<D>::SMEM;
     auto k = lin_pipe_kernel<D>;
     if (allow_smem(k, smem) != cudaSuccess) return LQ_ERR_CUDA;
-    const int grid = persistent_grid(k, kLpThreads, smem, a.work * a.nseg);
-    if (grid <= 0) return LQ_ERR_CUDA;
-    return launched(launch_pdl(k, grid, kLpThreads, smem, s, a, mq, mk, mv));
+    return launched(launch_pdl(k, a.work * a.nseg, kLpThreads, smem, s, a, mq, mk, mv));
 }
 
 // bf16 prompts from here on take the chunkwise form

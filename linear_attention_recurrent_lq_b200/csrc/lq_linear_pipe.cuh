@@ -11,8 +11,10 @@
 // before a token that would take G below 2^-64: 1 / G stays far inside FP32,
 // and a gate of 0 starts a chunk, where it clears the state exactly.
 //
-// One CTA per SM walks the work items (a head, or a segment of a prompt cut
-// along time) b, b + grid, ... as one stream of chunks.  The state is an FP32
+// There is a CTA for each work item (a head, or a segment of a prompt cut along
+// time), but one that runs takes over the items of CTAs that have not started
+// (cluster launch control), so one CTA per SM sees a stream of chunks across
+// items, and prompts of unequal length keep all SMs busy.  The state is an FP32
 // accumulator in tensor memory (lane = value channel) onto which V^T K' is
 // summed.  The CTA's warps, one of each kind on every scheduler:
 //   0 .. 7   the state: scaled, and cut into the pieces of an A operand in
@@ -59,7 +61,7 @@ struct LpShape {
     static constexpr uint32_t V = KB * 16384u, STAGE = KB * 24576u;
     static constexpr uint32_t P = ST * STAGE, K = P + 3u * 8192u, KBUF = 3u * KB * 8192u, RING = K + NK * KBUF;
     static constexpr uint32_t BAR = RING + kLpRing * (uint32_t)sizeof(LpSlot);
-    static constexpr uint32_t SMEM = BAR + 256u + 1024u;
+    static constexpr uint32_t CLAIM = BAR + 256u, SMEM = CLAIM + 16u + 1024u;
     // state warps at work: all, or those whose lanes are < 64
     static constexpr int SW = D / 16;
 };
@@ -68,9 +70,32 @@ struct LpBars {
     uint64_t full[4], empty[4], ring_full[kLpRing], ring_free[kLpRing];
     uint64_t qk_done, p_ready, s_ready, y_done, k_ready[2], d_done[2], o_done[2], o_free[2];
     uint32_t tmem, chunks;  // chunks: how many there are, once the feeder knows
+    uint64_t claim_done;
     uint32_t from_zero[4];  // per stage: the chunk starts from a zero state
 };
 static_assert(sizeof(LpBars) <= 256, "barrier space");
+
+// Ask for a CTA of this grid that has not started; the answer (16 bytes)
+// arrives on `bar`.  Not to be asked again after a refusal.
+__device__ __forceinline__ void claim_cta(uint32_t answer, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, 16u);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(answer), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ int claimed_cta(uint32_t answer) {  // -1: none is left
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(x) : "r"(answer) : "memory");
+    return got ? (int)x : -1;
+}
+
+__device__ __forceinline__ void lin_give_up(const LinArgs &A, int it) {
+    const int w = it / A.nseg, bi = w >= 0 && w < A.work ? A.map.blob(w) : -1;
+    if (bi >= 0) set_status(A.state + (size_t)bi * A.L.blob, LQ_DEV_TIMEOUT);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kLpThreads, 1)
@@ -92,6 +117,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             mbar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < kLpRing; ++i) {
+            ring[i].flags = kLpEnd;
             mbar_init(&bars->ring_full[i], 1);
             mbar_init(&bars->ring_free[i], SH::SW + 14);  // output, key and score warps too
         }
@@ -106,6 +132,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             mbar_init(&bars->o_free[i], 4);
         }
         bars->chunks = 0xFFFFFFFFu;
+        mbar_init(&bars->claim_done, 1);
         fence_mbar_init();
     }
     pdl_wait();
@@ -116,7 +143,6 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int items = A.work * A.nseg;
 
     bool ok = true;  // false: a wait gave up; every role then leaves
     auto wait = [&](uint64_t *b, uint32_t phase) {
@@ -130,13 +156,21 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 
     if (warp == 19) {
         // ------------------------------------------------------- the feeder
-        uint32_t r = 0, c = 0;
+        uint32_t r = 0, c = 0, claims = 0;
         auto slot_wait = [&]() -> LpSlot * {
             if (r >= kLpRing) wait(&bars->ring_free[r % kLpRing], r / kLpRing - 1u);
             return ring + r % kLpRing;
         };
 #pragma unroll 1
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        for (int it = blockIdx.x, next = it; it >= 0 && ok; it = next) {
+            // the next item, while this one is fed
+            if (lane == 0) claim_cta(base + SH::CLAIM, &bars->claim_done);
+            auto claimed = [&]() {
+                wait(&bars->claim_done, claims++);
+                next = claimed_cta(base + SH::CLAIM);
+                fence_async_smem();  // the answer has been read before the next one is written
+                __syncwarp();
+            };
             const int w = it / A.nseg, seg = it - w * A.nseg;
             const int row = w / A.map.heads, hh = w - row * A.map.heads;
             const int len = lin_length(A, row), last = lin_last_segment(A, len);
@@ -167,6 +201,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 }
                 arrive(&bars->ring_full[r % kLpRing]);
                 ++r;
+                claimed();
                 continue;
             }
             const float *src = lin_state_source(A, w, seg, blob);
@@ -233,6 +268,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 } else {
                     a0 = gate(t0 + 2 * lane); a1 = gate(t0 + 2 * lane + 1); a64 = gate(t0 + C);
                 }
+            }
+            claimed();
+            if (!ok && lane == 0) {  // claimed, but not to be done
+                lin_give_up(A, it);
+                if (next >= 0) lin_give_up(A, next);
             }
         }
         LpSlot *sl = slot_wait();
@@ -561,11 +601,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             }
             arrive(&bars->ring_free[r % kLpRing]);
         }
-        if (!ok && lane == 0)  // this item and those behind it are not done
-            for (int x = blockIdx.x; x < items; x += gridDim.x) {
-                const int bi = x / A.nseg >= w ? A.map.blob(x / A.nseg) : -1;
-                if (bi >= 0) set_status(A.state + (size_t)bi * A.L.blob, LQ_DEV_TIMEOUT);
-            }
+        if (!ok && lane == 0) {  // the items that are described may not be done
+            lin_give_up(A, w * A.nseg);
+            for (int i = 0; i < kLpRing; ++i)
+                if (!(ring[i].flags & kLpEnd)) lin_give_up(A, ring[i].w * A.nseg);
+        }
     }
     tc_fence_before();
     __syncthreads();

@@ -9,29 +9,32 @@
 // last to the first, with the product of the gates behind them carried along
 // (a gate of 0 is exact).  W k is cut into three bf16 pieces.
 //
-// One CTA takes one (head, segment): eight warps weight the keys, one thread
-// issues the products, one warp feeds (gates, TMA).  Bound by HBM: 516 bytes
-// per token and head (d = 128), 1390 clocks per chunk and SM; 768 are tensor
-// time.
+// One CTA takes one (head, segment): two groups of eight warps weight the keys
+// of even and of odd chunks (one after the other, all sixteen: 2400 clocks per
+// chunk, the latency of that work), one thread issues the products, one warp
+// feeds (gates, TMA).  Bound by HBM: 516 bytes per token and head (d = 128),
+// 1390 clocks per chunk and SM; 768 are tensor time.
 #pragma once
 
 #include "lq_linear_mma.cuh"
 
 namespace lq {
 
-constexpr int kLsThreads = 10 * 32;
+constexpr int kLsKeys = 16;  // warps that weight the keys
+constexpr int kLsThreads = (kLsKeys + 2) * 32;
 constexpr int kLsStages = 3;
+constexpr int kLsGates = 8;  // chunks of gates on their way (a gate is a memory latency of its own)
 
 template <int D>
 struct LsShape {
     static constexpr int KB = D / 64;
     // a stage: K and V, KB blocks of 64 rows x 128 bytes each
     static constexpr uint32_t V = KB * 8192u, STAGE = 2u * V, K = kLsStages * STAGE, KBUF = 3u * KB * 8192u;
-    static constexpr uint32_t W = K + 2u * KBUF, BAR = W + kLsStages * 256u, SMEM = BAR + 128u + 1024u;
+    static constexpr uint32_t W = K + 2u * KBUF, G = W + kLsStages * 256u, BAR = G + kLsGates * 256u, SMEM = BAR + 128u + 1024u;
 };
 
 struct LsBars {
-    uint64_t full[kLsStages], empty[kLsStages], k_ready[2], d_done[2];
+    uint64_t full[kLsStages], empty[kLsStages], k_ready[2], d_done[2], all_done;
     uint32_t tmem;
 };
 static_assert(sizeof(LsBars) <= 128, "barrier space");
@@ -54,8 +57,9 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             mbar_init(&bars->full[i], 1);
             mbar_init(&bars->empty[i], 1);
         }
+        mbar_init(&bars->all_done, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->k_ready[i], 8);
+            mbar_init(&bars->k_ready[i], kLsKeys / 2);
             mbar_init(&bars->d_done[i], 1);
         }
         fence_mbar_init();
@@ -64,7 +68,7 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     pdl_trigger();
     // a segment before the one that holds the prompt's end is whole
     if (A.map.blob(w) < 0 || seg >= lin_last_segment(A, lin_length(A, row))) return;  // uniform: not needed
-    if (warp == 8) tmem_alloc(&bars->tmem, 128u);
+    if (warp == kLsKeys) tmem_alloc(&bars->tmem, 128u);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -75,20 +79,40 @@ __global__ void __launch_bounds__(kLsThreads, 1)
         if (!mbar_try_wait(b, phase & 1u) && !mbar_wait_bounded(b, phase & 1u)) ok = false;
     };
 
-    if (warp == 9) {  // the feeder
+    if (warp == kLsKeys + 1) {  // the feeder
         const float *gates = A.decay + lin_v_row(A, row, hh, t_begin);
         const size_t gs = (size_t)A.map.heads;
         const int x = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens + t_begin;
         float carry = 1.f;  // product of the gates behind the chunk
         int bad = kNoBad;
-        auto gate = [&](int t) -> float { return t >= 0 ? __ldcg(gates + (size_t)t * gs) : 1.f; };
-        float a0 = gate((chunks - 1) * C + 2 * lane), a1 = gate((chunks - 1) * C + 2 * lane + 1);
+        auto ask = [&](int i) {  // gates of the i-th chunk from the end
+            if (i < chunks) {
+                const float *g = gates + (size_t)((chunks - 1 - i) * C + 2 * lane) * gs;
+                uint8_t *to = smem + SH::G + (i % kLsGates) * 256 + 8 * lane;
+                cp_async4(to, g, true);
+                cp_async4(to + 4, g + gs, true);
+            }
+            cp_async_commit();
+        };
+        for (int i = 0; i < kLsGates - 1; ++i) ask(i);
 #pragma unroll 1
         for (int i = 0; i < chunks && ok; ++i) {
             const int at = (chunks - 1 - i) * C;
             const uint32_t st = (uint32_t)i % kLsStages;
             if (i >= kLsStages) wait(&bars->empty[st], (uint32_t)i / kLsStages - 1u);
-            const float n0 = gate(at - C + 2 * lane), n1 = gate(at - C + 2 * lane + 1);
+            if (lane == 0 && ok) {  // the loads first, the weights while they are under way
+                uint8_t *sp = smem + st * SH::STAGE;
+                mbar_expect_tx(&bars->full[st], SH::STAGE);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    tma_load_2d(sp + kb * 8192, &mk, x + 64 * kb, y0 + at, &bars->full[st]);
+                    tma_load_2d(sp + SH::V + kb * 8192, &mv, xv + 64 * kb, y0 + at, &bars->full[st]);
+                }
+            }
+            ask(i + kLsGates - 1);
+            cp_async_wait<kLsGates - 1>();  // a lane reads what it asked for
+            const float2 a = *reinterpret_cast<const float2 *>(smem + SH::G + (i % kLsGates) * 256 + 8 * lane);
+            const float a0 = a.x, a1 = a.y;
             const unsigned w0 = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(a0));
             const unsigned w1 = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(a1));
             if (w0 | w1) bad = t_begin + at + min(w0 ? 2 * (__ffs(w0) - 1) : C, w1 ? 2 * (__ffs(w1) - 1) + 1 : C);
@@ -103,23 +127,13 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             *reinterpret_cast<float2 *>(smem + SH::W + st * 256u + 8u * lane) = make_float2(a1 * b1, b1);
             carry *= __shfl_sync(0xFFFFFFFFu, suf, 0);
             __syncwarp();
-            if (lane == 0 && ok) {
-                uint8_t *sp = smem + st * SH::STAGE;
-                mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    tma_load_2d(sp + kb * 8192, &mk, x + 64 * kb, y0 + at, &bars->full[st]);
-                    tma_load_2d(sp + SH::V + kb * 8192, &mv, xv + 64 * kb, y0 + at, &bars->full[st]);
-                }
-            }
-            a0 = n0;
-            a1 = n1;
+            if (lane == 0) mbar_arrive(&bars->full[st]);
         }
         if (lane == 0) {
             A.ws_g[(size_t)w * A.nseg + seg] = carry;
             A.ws_bad[(size_t)w * A.nseg + seg] = bad;
         }
-    } else if (warp == 8) {  // the issuer: S^T += V^T K'
+    } else if (warp == kLsKeys) {  // the issuer: S^T += V^T K'
         auto uni = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
         constexpr uint32_t id = lc_idesc(128, D, 1, 1), vlbo = KB > 1 ? 8192u : 0u;
         const uint32_t v0 = uni(lc_desc(base + SH::V, vlbo)), k0 = uni(lc_desc(base + SH::K, 8192u)), td = uni(tmem);
@@ -138,19 +152,20 @@ __global__ void __launch_bounds__(kLsThreads, 1)
                                   x < 2 || ks > 0 ? 1u : acc);
                 umma_commit(&bars->d_done[i & 1]);
                 umma_commit(&bars->empty[i % kLsStages]);
+                if (i == chunks - 1) umma_commit(&bars->all_done);
             }
             __syncwarp();
         }
     } else {  // the keys, then the state to the workspace
         constexpr int NP = 8 * KB;
 #pragma unroll 1
-        for (int i = 0; i < chunks && ok; ++i) {
+        for (int i = warp / (kLsKeys / 2); i < chunks && ok; i += 2) {
             const uint32_t st = (uint32_t)i % kLsStages;
             wait(&bars->full[st], (uint32_t)i / kLsStages);
             if (i >= 2) wait(&bars->d_done[i & 1], (uint32_t)i / 2u - 1u);
             const float *W = reinterpret_cast<const float *>(smem + SH::W + st * 256u);
 #pragma unroll 2
-            for (int x = tid; x < C * NP; x += 256) {
+            for (int x = tid % (kLsKeys * 16); x < C * NP; x += kLsKeys * 16) {
                 const int t = x / NP, pc = x % NP;
                 const uint32_t o = lc_tile_off(t, pc, 8192u);
                 lc_weighted_piece(*reinterpret_cast<const uint4 *>(smem + st * SH::STAGE + o), W[t],
@@ -160,15 +175,16 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->k_ready[i & 1]);
         }
-        wait(&bars->d_done[(chunks - 1) & 1], (uint32_t)(chunks - 1) / 2u);
+        wait(&bars->all_done, 0u);
         tc_fence_after();
-        const int j = 32 * (warp & 3) + lane, half = warp >> 2;
+        constexpr int Q = D / (kLsKeys / 4);  // key channels of a warp
+        const int j = 32 * (warp & 3) + lane, i0 = Q * (warp >> 2);
         if ((warp & 3) < D / 32) {
-            float *dst = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D) + (size_t)(D / 2 * half) * D + j;
-#pragma unroll 1
-            for (int x = 0; x < D / 2; x += 16) {
+            float *dst = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D) + (size_t)i0 * D + j;
+#pragma unroll
+            for (int x = 0; x < Q; x += 16) {
                 uint32_t v[16];
-                tmem_ld16_async(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(D / 2 * half + x), v);
+                tmem_ld16_async(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(i0 + x), v);
                 tmem_ld_wait(v);
 #pragma unroll
                 for (int y = 0; y < 16; ++y) dst[(size_t)(x + y) * D] = __uint_as_float(v[y]);
@@ -178,7 +194,7 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tmem, 128u);
+    if (warp == kLsKeys) tmem_dealloc(tmem, 128u);
 }
 
 }  // namespace lq
