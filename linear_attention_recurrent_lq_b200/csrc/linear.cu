@@ -209,12 +209,12 @@ lq_status check_linear_slots(const lq_config *cfg, const void *state, const int3
 
 template <int D, bool BF16>
 cudaError_t launch_qk_norm(QkNormArgs a, cudaStream_t s) {
-    constexpr int LR = D / (BF16 ? 8 : 4), per = 256 / LR * kNormUnroll;
-    const long long nb = (2 * a.qk_rows + per - 1) / per;
-    const long long gates = a.kda ? a.heads_n * LR : a.heads_n;
-    const long long ng = (gates + 255) / 256;
+    constexpr int G = 256 / (D / (BF16 ? 8 : 4));  // rows a block takes at once
+    const long long nb = (2 * a.qk_rows + G * kNormUnroll - 1) / (G * kNormUnroll);
+    const long long per = a.kda ? G * kGateUnroll : 256, ng = (a.heads_n + per - 1) / per;
     if (nb + ng > 0x7FFFFFFF) return cudaErrorInvalidValue;
     a.norm_blocks = (unsigned)nb;
+    a.gate_blocks = (unsigned)ng;
     return launch_pdl(qk_norm_kernel<D, BF16>, (int)(nb + ng), 256, 0u, s, a);
 }
 
@@ -292,7 +292,7 @@ lq_status lq_qk_norm(const lq_config *cfg, int rows, int qk_heads, const void *q
         return LQ_ERR_MISALIGNED;
     if (rows == 0) return LQ_OK;
     QkNormArgs n{q, k, a, b, a_log, dt_bias, q_out, k_out, decay, beta, q_scale, eps, (long long)rows * qk_heads,
-                 (long long)rows * c.num_heads, c.num_heads, c.decay_kind, 0u};
+                 (unsigned)(rows * c.num_heads), c.num_heads, c.decay_kind, 0u, 0u};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (c.dk == 128)
         return launched(c.in_dtype ? launch_qk_norm<128, true>(n, s) : launch_qk_norm<128, false>(n, s));

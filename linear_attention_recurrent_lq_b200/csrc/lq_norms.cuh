@@ -23,25 +23,10 @@ struct QkNormArgs {
     float *decay, *beta;
     float q_scale, eps;
     long long qk_rows;  // rows * Hk
-    long long heads_n;  // rows * H
+    unsigned heads_n;   // rows * H
     int H, kda;
-    unsigned norm_blocks;  // the first blocks take q and k rows, the others the gates
+    unsigned norm_blocks, gate_blocks;  // blocks for q and k rows, and for the gates
 };
-
-template <bool BF16>
-__device__ __forceinline__ void load_piece(const void *p, float (&x)[BF16 ? 8 : 4]) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        } else {
-            x[i] = __uint_as_float(u[i]);
-        }
-    }
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
@@ -59,78 +44,121 @@ __device__ __forceinline__ void store_piece(void *p, const float (&x)[BF16 ? 8 :
     *reinterpret_cast<uint4 *>(p) = w;
 }
 
-// exp(-rate softplus(x)); softplus by log1p, so that small ones keep their digits
+// exp(-rate softplus(x)), softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|).
+// Small ones have to keep their digits, so log(1 + e) is not taken of a rounded
+// 1 + e but from its series 2 artanh(r), r = e / (2 + e) <= 1/3; the first
+// term left out is r^14 / 15 <= 1.4e-8 of the sum.  20 instructions; with
+// log1pf, expf and their branches the gates of a key-channel layer took as
+// long as its memory traffic twice.
 __device__ __forceinline__ float gate_decay(float x, float rate) {
-    const float soft = fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-    return expf(-rate * soft);
+    const float e = __expf(-fabsf(x));
+    const float r = __fdividef(e, 2.f + e), r2 = r * r;
+    float p = fmaf(r2, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(r2, p, 1.f / 9.f);
+    p = fmaf(r2, p, 1.f / 7.f);
+    p = fmaf(r2, p, 1.f / 5.f);
+    p = fmaf(r2, p, 1.f / 3.f);
+    p = fmaf(r2, p, 1.f);
+    return __expf(-rate * (fmaxf(x, 0.f) + 2.f * r * p));
 }
 
 __device__ __forceinline__ float sigmoidf(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
+// the same within 1e-6: an output gate is rounded with y once more
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-constexpr int kNormUnroll = 4;
+template <bool BF16>
+__device__ __forceinline__ void unpack_piece(const uint4 &w, float (&x)[BF16 ? 8 : 4]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        } else {
+            x[i] = __uint_as_float(u[i]);
+        }
+    }
+}
+
+// Pieces of 16 bytes a thread loads before it uses the first: 8 for q and k
+// rows, 4 for the gates of key channels (4 and 1: 95 us for 16384 tokens of 12
+// heads, d = 128, 54 us of memory traffic).
+constexpr int kNormUnroll = 8, kGateUnroll = 4;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) qk_norm_kernel(QkNormArgs A) {
     constexpr int V = BF16 ? 8 : 4, E = BF16 ? 2 : 4, LR = D / V;  // values and lanes per row piece
-    const int tid = threadIdx.x;
+    constexpr int G = 256 / LR;                                    // rows per pass of the block
+    const int tid = threadIdx.x, c = (tid % LR) * V;
+    // the two kinds of block alternate over the grid, so that an SM has the one
+    // bound by memory and the one bound by its exponentials at the same time
+    const unsigned blocks = A.norm_blocks + A.gate_blocks;
+    const unsigned gates = (unsigned)((unsigned long long)blockIdx.x * A.gate_blocks / blocks);  // before this block
+    const bool is_gate = (unsigned)((unsigned long long)(blockIdx.x + 1u) * A.gate_blocks / blocks) > gates;
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x < A.norm_blocks) {
-        constexpr int G = 256 / LR;  // rows per pass of the block
-        const long long r0 = (long long)blockIdx.x * (G * kNormUnroll) + tid / LR;
-        const int c = tid % LR;
-        float x[kNormUnroll][V];
+    if (!is_gate) {
+        const long long r0 = (long long)(blockIdx.x - gates) * (G * kNormUnroll) + tid / LR;
+        uint4 w[kNormUnroll];
 #pragma unroll
         for (int u = 0; u < kNormUnroll; ++u) {
             const long long r = r0 + u * G;
-            if (r < 2 * A.qk_rows) {
-                const bool isk = r >= A.qk_rows;
-                const size_t o = ((size_t)(isk ? r - A.qk_rows : r) * D + c * V) * E;
-                load_piece<BF16>(static_cast<const uint8_t *>(isk ? A.k : A.q) + o, x[u]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[u][i] = 0.f;
-            }
+            const bool isk = r >= A.qk_rows;
+            const size_t o = ((size_t)(isk ? r - A.qk_rows : r) * D + c) * E;
+            w[u] = r < 2 * A.qk_rows ? __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(isk ? A.k : A.q) + o))
+                                     : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kNormUnroll; ++u) {
-            float ss = 0.f;
+            float x[V], ss = 0.f;
+            unpack_piece<BF16>(w[u], x);
 #pragma unroll
-            for (int i = 0; i < V; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+            for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
             for (int off = LR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
             const long long r = r0 + u * G;
             const bool isk = r >= A.qk_rows;
-            const float f = __fdiv_rn(isk ? 1.f : A.q_scale, __fsqrt_rn(ss + A.eps));
+            const float f = (isk ? 1.f : A.q_scale) * rsqrtf(ss + A.eps);
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[u][i] *= f;
+            for (int i = 0; i < V; ++i) x[i] *= f;
             if (r < 2 * A.qk_rows) {
-                const size_t o = ((size_t)(isk ? r - A.qk_rows : r) * D + c * V) * E;
-                store_piece<BF16>(static_cast<uint8_t *>(isk ? A.k_out : A.q_out) + o, x[u]);
+                const size_t o = ((size_t)(isk ? r - A.qk_rows : r) * D + c) * E;
+                store_piece<BF16>(static_cast<uint8_t *>(isk ? A.k_out : A.q_out) + o, x);
             }
         }
         return;
     }
-    const long long x = (long long)(blockIdx.x - A.norm_blocks) * 256 + tid;
     if (A.kda) {  // V channels of one head
-        const long long hr = x / LR;
-        if (hr >= A.heads_n) return;
-        const int h = (int)(hr % A.H), c = (int)(x % LR) * V;
-        float av[V];
-        load_piece<BF16>(static_cast<const uint8_t *>(A.a) + ((size_t)hr * D + c) * E, av);
-        const float rate = expf(A.a_log[h]);
+        const unsigned r0 = gates * (G * kGateUnroll) + tid / LR;  // rows * H < 2^31
+        uint4 w[kGateUnroll];
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 d = *reinterpret_cast<const float4 *>(A.dt_bias + (size_t)h * D + c + i);
-            const float4 g = make_float4(gate_decay(av[i] + d.x, rate), gate_decay(av[i + 1] + d.y, rate),
-                                         gate_decay(av[i + 2] + d.z, rate), gate_decay(av[i + 3] + d.w, rate));
-            *reinterpret_cast<float4 *>(A.decay + (size_t)hr * D + c + i) = g;
+        for (int u = 0; u < kGateUnroll; ++u) {
+            const unsigned r = r0 + u * G;
+            w[u] = r < A.heads_n ? __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.a) + ((size_t)r * D + c) * E))
+                                 : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (c == 0) A.beta[hr] = sigmoidf(load_in(A.b, (size_t)hr, BF16));
+#pragma unroll
+        for (int u = 0; u < kGateUnroll; ++u) {
+            const unsigned r = r0 + u * G;
+            if (r >= A.heads_n) return;
+            const unsigned h = r % (unsigned)A.H;
+            const float rate = __expf(A.a_log[h]);
+            float x[V];
+            unpack_piece<BF16>(w[u], x);
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 d = __ldg(reinterpret_cast<const float4 *>(A.dt_bias + (size_t)h * D + c + i));
+                const float4 g = make_float4(gate_decay(x[i] + d.x, rate), gate_decay(x[i + 1] + d.y, rate),
+                                             gate_decay(x[i + 2] + d.z, rate), gate_decay(x[i + 3] + d.w, rate));
+                *reinterpret_cast<float4 *>(A.decay + (size_t)r * D + c + i) = g;
+            }
+            if (c == 0) A.beta[r] = sigmoidf(load_in(A.b, (size_t)r, BF16));
+        }
         return;
     }
+    const unsigned x = gates * 256u + tid;
     if (x >= A.heads_n) return;
-    const int h = (int)(x % A.H);
+    const unsigned h = x % (unsigned)A.H;
     A.decay[x] = gate_decay(load_in(A.a, (size_t)x, BF16) + A.dt_bias[h], expf(A.a_log[h]));
     A.beta[x] = sigmoidf(load_in(A.b, (size_t)x, BF16));
 }
@@ -170,12 +198,12 @@ __global__ void __launch_bounds__(256) out_norm_kernel(OutNormArgs A) {
             if constexpr (GATE != kGateNone) {
                 const uint8_t *gp = static_cast<const uint8_t *>(A.gate) + o * E;
                 if constexpr (BF16) {
-                    load_piece<true>(gp, g[u]);
+                    unpack_piece<true>(__ldcs(reinterpret_cast<const uint4 *>(gp)), g[u]);
                 } else {
                     float h[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 4) {
-                        load_piece<false>(gp + 4 * i, h);
+                        unpack_piece<false>(__ldcs(reinterpret_cast<const uint4 *>(gp + 4 * i)), h);
                         g[u][i] = h[0]; g[u][i + 1] = h[1]; g[u][i + 2] = h[2]; g[u][i + 3] = h[3];
                     }
                 }
@@ -198,12 +226,12 @@ __global__ void __launch_bounds__(256) out_norm_kernel(OutNormArgs A) {
         for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
 #pragma unroll
         for (int off = LR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-        const float f = __fdiv_rn(1.f, __fsqrt_rn(fmaf(ss, 1.f / D, A.eps)));
+        const float f = rsqrtf(fmaf(ss, 1.f / D, A.eps));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float y = x[u][i] * f * w[i];
-            if constexpr (GATE == kGateSilu) y *= g[u][i] * sigmoidf(g[u][i]);
-            if constexpr (GATE == kGateSigmoid) y *= sigmoidf(g[u][i]);
+            if constexpr (GATE == kGateSilu) y *= g[u][i] * sigmoid_fast(g[u][i]);
+            if constexpr (GATE == kGateSigmoid) y *= sigmoid_fast(g[u][i]);
             x[u][i] = y;
         }
         const long long r = r0 + u * G;
