@@ -24,8 +24,8 @@
 //            memory
 //   16, 17, 21  the scores Q K^T, a block of 32 x 32 each: from tensor memory,
 //            times 1 / G, masked, in three pieces to shared memory
-//   18       one thread issues every product, in the order V^T P^T of chunk
-//            c - 1, then Q K^T, V^T K' and S^T Q^T of chunk c
+//   18       one thread issues V^T K', S^T Q^T and V^T P^T
+//   24       one thread issues Q K^T, ahead of them
 //   19       the feeder: gates and their products, the chunk's bounds, and the
 //            TMA loads
 // They meet in mbarriers only.  A barrier's waiters look at the parity of a
@@ -37,7 +37,7 @@
 
 namespace lq {
 
-constexpr int kLpThreads = 24 * 32;
+constexpr int kLpThreads = 25 * 32;
 constexpr int kLpRing = 4;     // chunk descriptions
 constexpr float kLpMinGate = 0x1p-64f;
 // tensor memory: Q K^T | O^T, two | S pieces | S
@@ -61,19 +61,19 @@ struct LpShape {
     static constexpr uint32_t V = KB * 16384u, STAGE = KB * 24576u;
     static constexpr uint32_t P = ST * STAGE, K = P + 3u * 8192u, KBUF = 3u * KB * 8192u, RING = K + NK * KBUF;
     static constexpr uint32_t BAR = RING + kLpRing * (uint32_t)sizeof(LpSlot);
-    static constexpr uint32_t CLAIM = BAR + 256u, SMEM = CLAIM + 16u + 1024u;
+    static constexpr uint32_t CLAIM = BAR + 320u, SMEM = CLAIM + 16u + 1024u;
     // state warps at work: all, or those whose lanes are < 64
     static constexpr int SW = D / 16;
 };
 
 struct LpBars {
     uint64_t full[4], empty[4], ring_full[kLpRing], ring_free[kLpRing];
-    uint64_t qk_done, p_ready, s_ready, y_done, k_ready[2], d_done[2], o_done[2], o_free[2];
+    uint64_t qk_done, qk_free, p_ready, s_ready, y_done, k_ready[2], d_done[2], o_done[2], o_free[2];
     uint32_t tmem, chunks;  // chunks: how many there are, once the feeder knows
     uint64_t claim_done;
     uint32_t from_zero[4];  // per stage: the chunk starts from a zero state
 };
-static_assert(sizeof(LpBars) <= 256, "barrier space");
+static_assert(sizeof(LpBars) <= 320, "barrier space");
 
 // Ask for a CTA of this grid that has not started; the answer (16 bytes)
 // arrives on `bar`.  Not to be asked again after a refusal.
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             mbar_init(&bars->ring_free[i], SH::SW + 14);  // output, key and score warps too
         }
         mbar_init(&bars->qk_done, 1);
+        mbar_init(&bars->qk_free, 3);
         mbar_init(&bars->p_ready, 3);
         mbar_init(&bars->s_ready, SH::SW);
         mbar_init(&bars->y_done, 1);
@@ -276,49 +277,39 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             }
         }
         LpSlot *sl = slot_wait();
-        if (lane == 0) sl->flags = kLpEnd;
+        if (lane == 0) {
+            sl->flags = kLpEnd;
+            bars->chunks = c;
+        }
         arrive(&bars->ring_full[r % kLpRing]);
         // what has been asked for lands before the CTA leaves
         for (uint32_t i = c >= ST ? c - ST + 1u : 0u; i < c; ++i) wait(&bars->full[i % ST], i / ST);
         if (c >= ST) wait(&bars->empty[c % ST], c / ST - 1u);
-        if (lane == 0) bars->chunks = c;
-        arrive(&bars->full[c % ST]);  // the issuer learns the end here
-    } else if (warp == 18) {
-        // ------------------------------------------------------- the issuer
+        arrive(&bars->full[c % ST]);  // warp 24 learns the end here
+    } else if (warp == 18 || warp == 24) {
+        // ------------------------------------------------------ the issuers
         constexpr uint32_t id64 = lc_idesc(128, 64, 0, 0), idpv = lc_idesc(128, 64, 1, 0),
                            idpv2 = lc_idesc(128, 32, 1, 0), idd = lc_idesc(128, D, 1, 1);
         constexpr uint32_t vlbo = KB > 1 ? 8192u : 0u;  // D = 64: lanes 64 .. repeat the others
         // A tcgen05.mma takes its operands' descriptions from uniform registers:
         // the bases pass through a shuffle, so that the compiler sees them as
-        // such and adds to them there.  This warp gets a sixth of a scheduler's
-        // slots: what it executes per product bounds the kernel.
+        // such and adds to them there.  An issuer gets a sixth of its scheduler's
+        // slots, and its products run hardly behind it: what it executes per
+        // product and per wait counts (descriptions built one by one: 140 clocks
+        // a product, 40 now).
         auto uni = [](uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); };
-        const uint32_t pd = uni(lc_desc(base + SH::P, 16u)), td = uni(tmem);
-        const uint32_t q0 = uni(lc_desc(base, 16u)), v0 = uni(lc_desc(base + SH::V, vlbo)), k0 = uni(lc_desc(base + SH::K, 8192u));
-        uint32_t c = 0, st = 0, full_ph = 0, acc = 1, before = 0;  // before: 16-byte units to the stage of chunk c - 1
+        const uint32_t td = uni(tmem), q0 = uni(lc_desc(base, 16u));
+        const volatile uint32_t *chunks = &bars->chunks;
+        uint32_t c = 0, st = 0, full_ph = 0;
+        if (warp == 24) {
 #pragma unroll 1
-        for (; ok; ++c) {
-            wait(&bars->full[st], full_ph);
-            if (c > 0) wait(&bars->p_ready, c - 1u);
-            if (!ok) break;
-            const bool more = c < *reinterpret_cast<volatile uint32_t *>(&bars->chunks);
-            const uint32_t at = uni(st * (SH::STAGE / 16u)), prev = uni(before);
-            const uint32_t acc_prev = uni(acc);  // whether O^T of chunk c - 1 holds S^T Q^T
-            const uint32_t o_prev = uni(td + kLpO + 64u * ((c & 1u) ^ 1u)), o = uni(td + kLpO + 64u * (c & 1u));
-            if (lc_elect()) {
-                tc_fence_after();
-                if (c > 0) {  // O^T += V^T P^T of chunk c - 1
-#pragma unroll
-                    for (int x = 2; x >= 0; --x)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)  // tokens 32 .. reach rows 32 .. only
-                            lc_mma_ss(ks < 2 ? o_prev : o_prev + 32u, v0 + prev + ks * 128u,
-                                      pd + x * 512u + (ks < 2 ? 0u : 256u) + ks * 2u,
-                                      (ks < 2 ? idpv : idpv2) | (x == 1 ? kLcNegB : 0u), x < 2 || ks > 0 ? 1u : acc_prev);
-                    umma_commit(&bars->o_done[(c & 1u) ^ 1u]);
-                    umma_commit(&bars->empty[st == 0u ? ST - 1 : st - 1u]);
-                }
-                if (more) {  // Q K^T; rows 64 .. 127 (K K^T) are not used
+            for (; ok; ++c) {
+                const uint32_t at = uni(st * (SH::STAGE / 16u));
+                wait(&bars->full[st], full_ph);
+                if (c > 0) wait(&bars->qk_free, c - 1u);
+                if (!ok || c >= *chunks) break;
+                if (lc_elect()) {  // Q K^T; rows 64 .. 127 (K K^T) are not used
+                    tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint32_t qd = q0 + at + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u;
@@ -326,44 +317,65 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     }
                     umma_commit(&bars->qk_done);
                 }
+                __syncwarp();
+                if (++st == (uint32_t)ST) {
+                    st = 0;
+                    full_ph ^= 1u;
+                }
             }
-            __syncwarp();
-            if (!more) break;
-            wait(&bars->k_ready[c % NK], c / NK);
-            wait(&bars->s_ready, c);
-            if (!ok) break;
-            const uint32_t kd = uni(k0 + (c % NK) * (SH::KBUF / 16u));
-            acc = uni(*reinterpret_cast<volatile uint32_t *>(&bars->from_zero[st])) ? 0u : 1u;
-            if (lc_elect()) {
-                tc_fence_after();
+        } else {
+            const uint32_t pd = uni(lc_desc(base + SH::P, 16u)), v0 = uni(lc_desc(base + SH::V, vlbo)),
+                           k0 = uni(lc_desc(base + SH::K, 8192u));
+#pragma unroll 1
+            for (; ok; ++c) {
+                const uint32_t at = uni(st * (SH::STAGE / 16u)), o = uni(td + kLpO + 64u * (c & 1u));
+                const uint32_t kd = uni(k0 + (c % NK) * (SH::KBUF / 16u));
+                wait(&bars->k_ready[c % NK], c / NK);  // the chunk's loads have landed, too
+                if (!ok || c >= *chunks) break;
+                const uint32_t acc = uni(*reinterpret_cast<volatile uint32_t *>(&bars->from_zero[st])) ? 0u : 1u;
+                wait(&bars->s_ready, c);
+                if (!ok) break;
+                if (lc_elect()) {
+                    tc_fence_after();
 #pragma unroll
-                for (int x = 2; x >= 0; --x)  // S += V^T K'
+                    for (int x = 2; x >= 0; --x)  // S += V^T K'
 #pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks)
-                        lc_mma_ss(td + kLpS, v0 + at + ks * 128u, kd + x * (KB * 512) + ks * 128u, idd | (x == 1 ? kLcNegB : 0u),
-                                  x < 2 || ks > 0 ? 1u : acc);
-                umma_commit(&bars->d_done[c % NK]);
-                if (acc) {  // S^T Q^T
+                        for (int ks = 0; ks < C / 16; ++ks)
+                            lc_mma_ss(td + kLpS, v0 + at + ks * 128u, kd + x * (KB * 512) + ks * 128u, idd | (x == 1 ? kLcNegB : 0u),
+                                      x < 2 || ks > 0 ? 1u : acc);
+                    umma_commit(&bars->d_done[c % NK]);
+                    if (acc) {  // S^T Q^T
+#pragma unroll
+                        for (int x = 2; x >= 0; --x)
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                lc_mma_ts(o, td + kLpSp + (uint32_t)(x * HD + 8 * ks),
+                                          q0 + at + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u,
+                                          id64 | (x == 1 ? kLcNegA : 0u), x < 2 || ks > 0);
+                    }
+                    umma_commit(&bars->y_done);
+                }
+                __syncwarp();
+                wait(&bars->p_ready, c);
+                if (!ok) break;
+                if (lc_elect()) {  // O^T += V^T P^T
+                    tc_fence_after();
 #pragma unroll
                     for (int x = 2; x >= 0; --x)
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            lc_mma_ts(o, td + kLpSp + (uint32_t)(x * HD + 8 * ks),
-                                  q0 + at + (uint32_t)(ks >> 2) * 1024u + (uint32_t)(ks & 3) * 2u, id64 | (x == 1 ? kLcNegA : 0u),
-                                  x < 2 || ks > 0);
+                        for (int ks = 0; ks < 4; ++ks)  // tokens 32 .. reach rows 32 .. only
+                            lc_mma_ss(ks < 2 ? o : o + 32u, v0 + at + ks * 128u, pd + x * 512u + (ks < 2 ? 0u : 256u) + ks * 2u,
+                                      (ks < 2 ? idpv : idpv2) | (x == 1 ? kLcNegB : 0u), x < 2 || ks > 0 ? 1u : acc);
+                    umma_commit(&bars->o_done[c & 1u]);
+                    umma_commit(&bars->empty[st]);
                 }
-                umma_commit(&bars->y_done);
-            }
-            __syncwarp();
-            before = at;
-            if (++st == (uint32_t)ST) {
-                st = 0;
-                full_ph ^= 1u;
+                __syncwarp();
+                if (++st == (uint32_t)ST) st = 0;
             }
         }
         // every product has ended before tensor memory is given back
-        if (c > 0) mbar_wait_bounded(&bars->o_done[(c - 1u) & 1u], ((c - 1u) / 2u) & 1u);
-    } else if (warp == 20 || warp >= 22 || (warp >= 8 && warp < 16 && (D == 128 ? warp >= 12 : (warp & 3) >= 2))) {
+        if (warp == 18 && c > 0) mbar_wait_bounded(&bars->o_done[(c - 1u) & 1u], ((c - 1u) / 2u) & 1u);
+    } else if (warp == 20 || warp == 22 || warp == 23 || (warp >= 8 && warp < 16 && (D == 128 ? warp >= 12 : (warp & 3) >= 2))) {
         // ------------------------------------------------- k / G, in pieces
         constexpr int NP = 8 * KB, NT = 7 * 32;
         const int kw = warp == 20 ? 4 : warp >= 22 ? warp - 17 : D == 128 ? warp - 12 : (warp & 1) + (warp >= 12 ? 2 : 0);
@@ -376,7 +388,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             const int flags = ok ? sl->flags : kLpEnd;
             if (flags & (kLpEnd | kLpNone)) {
                 arrive(&bars->ring_free[r % kLpRing]);
-                if (flags & kLpEnd) break;
+                if (flags & kLpEnd) {  // warp 18 learns it here
+                    if (c >= NK) wait(&bars->d_done[c % NK], c / NK - 1u);
+                    arrive(&bars->k_ready[c % NK]);
+                    break;
+                }
                 continue;
             }
             const int n = sl->n;
@@ -384,12 +400,19 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             wait(&bars->full[c % ST], c / ST);
             if (c >= NK) wait(&bars->d_done[c % NK], c / NK - 1u);
             if (ok) {
-#pragma unroll 2
-                for (int x = kt; x < C * NP; x += NT) {
-                    const int t = x / NP, pc = x % NP;
+                // NT is a multiple of NP: a thread keeps its piece of the row
+                constexpr int RS = NT / NP, R = (C + RS - 1) / RS;
+                const int pc = kt % NP, t0 = kt / NP;
+                const uint8_t *kp = sp + 8192 + (pc >> 3) * 16384;
+                uint8_t *dp = smem + SH::K + (c % NK) * SH::KBUF + (pc >> 3) * 8192;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int t = t0 + i * RS;
+                    if (i == R - 1 && t >= C) break;
+                    const uint32_t o = (uint32_t)(t * 128 + (((pc & 7) ^ (t & 7)) << 4));
                     uint4 kk = make_uint4(0u, 0u, 0u, 0u);  // rows behind the chunk
-                    if (t < n) kk = *reinterpret_cast<const uint4 *>(sp + 8192 + lc_tile_off(t, pc, 16384u));
-                    lc_weighted_piece(kk, sl->inv[t], smem + SH::K + (c % NK) * SH::KBUF + lc_tile_off(t, pc, 8192u), KB * 8192u);
+                    if (t < n) kk = *reinterpret_cast<const uint4 *>(kp + o);
+                    lc_weighted_piece(kk, sl->inv[t], dp + o, KB * 8192u);
                 }
                 // rows of V behind the chunk meet zeros of P and K', so they must be finite
                 for (int x = kt; x < (C - n) * NP; x += NT)
@@ -422,7 +445,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             tmem_ld16_async(tlane + kLpQK + (uint32_t)c0 + 16u, v[1]);
             tmem_ld_wait(v[0]);
             tmem_ld_wait(v[1]);
-            // (V^T P^T of the chunk before was issued before Q K^T: P is free)
+            tc_fence_before();
+            arrive(&bars->qk_free);
+            if (c > 0) wait(&bars->o_done[(c - 1u) & 1u], (c - 1u) / 2u);  // P is free
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -444,7 +469,6 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     *reinterpret_cast<uint4 *>(o + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             fence_async_smem();
-            tc_fence_before();
             arrive(&bars->p_ready);
             arrive(&bars->ring_free[r % kLpRing]);
             ++c;
