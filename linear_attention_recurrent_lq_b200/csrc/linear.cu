@@ -17,25 +17,53 @@ namespace {
 
 constexpr int kSms = 148;
 
-// A prompt is cut along time where its heads alone leave most SMs idle; a
-// segment has at least kMinSegment tokens.
-constexpr int kMinSegment = 256;
+// bf16 prompts from here on take the chunkwise form on the tensor cores
+constexpr int kMinChunked = 32;
+
+bool chunked(const lq_config &c, int tokens) { return c.in_dtype == 1 && tokens >= kMinChunked; }
+
+// Where the heads alone leave SMs idle, a prompt is cut along time into `nseg`
+// segments of `seg_len` tokens.  That costs a pass over k and v for what the
+// segments leave behind, and a scan over those states.
 constexpr int kMaxSegments = 64;
 
 struct Cut {
     int seg_len, nseg;
 };
 
-Cut cut_of(int64_t work, int tokens) {
-    Cut c{tokens > 0 ? tokens : 1, 1};
-    if (work <= 0 || work >= kSms || tokens < 2 * kMinSegment) return c;
-    int64_t n = (2 * kSms) / work;
-    if (n > tokens / kMinSegment) n = tokens / kMinSegment;
+Cut cut_of(const lq_config &c, int64_t work, int tokens) {
+    Cut best{tokens > 0 ? tokens : 1, 1};
+    if (work <= 0 || tokens < 256) return best;
+    if (chunked(c, tokens)) {
+        // One CTA per SM and kind of pass; time of a chunk of 64 tokens in the
+        // main pass, in the first pass, and of the launches and the scan, in
+        // units of 0.1 us as measured at d = 128
+        const int64_t main = 27, first = 12, fixed = 150;
+        auto cost = [&](int64_t n, int64_t chunks) {
+            const int64_t t = (work * n + kSms - 1) / kSms * chunks * main;
+            return n == 1 ? t : t + (work * (n - 1) + kSms - 1) / kSms * chunks * first + fixed;
+        };
+        const int64_t all = (tokens + 63) / 64;
+        int64_t least = cost(1, all);
+        for (int64_t n = 2; n <= kMaxSegments && n * 2 <= all; ++n) {
+            const int64_t chunks = (all + n - 1) / n, got = (all + chunks - 1) / chunks;
+            if (cost(got, chunks) < least) {
+                least = cost(got, chunks);
+                best = Cut{(int)(chunks * 64), (int)got};
+            }
+        }
+        return best;
+    }
+    // Token after token: three CTAs of 64 columns per SM, segments of 64 tokens
+    // or more
+    const int64_t ctas = work * (c.dv / 64);
+    int64_t n = 3 * kSms / ctas;
+    if (n > tokens / 64) n = tokens / 64;
     if (n > kMaxSegments) n = kMaxSegments;
-    if (n < 2) return c;
-    c.seg_len = (int)align_up((uint32_t)((tokens + n - 1) / n), 64u);
-    c.nseg = (tokens + c.seg_len - 1) / c.seg_len;
-    return c;
+    if (n < 2) return best;
+    best.seg_len = (int)align_up((uint32_t)((tokens + n - 1) / n), 16u);
+    best.nseg = (tokens + best.seg_len - 1) / best.seg_len;
+    return best;
 }
 
 // [work, nseg, dk, dv] f32 states | [work, nseg] gate products | [work, nseg]
@@ -142,15 +170,12 @@ lq_status launch_chunked(const LinArgs &a, cudaStream_t s) {
     return launched(launch_pdl(k, a.work * a.nseg, kLpThreads, smem, s, a, mq, mk, mv));
 }
 
-// bf16 prompts from here on take the chunkwise form
-constexpr int kMinChunked = 32;
-
 template <int D, bool BF16>
-lq_status launch_prefill(const LinArgs &a, cudaStream_t s) {
+lq_status launch_prefill(const LinArgs &a, bool on_tensor_cores, cudaStream_t s) {
     if constexpr (BF16)
-        if (a.tokens >= kMinChunked) return launch_chunked<D>(a, s);
-    // few heads: 16 columns per CTA, else 64
-    if ((int64_t)a.work * a.nseg * (D / 64) < 2 * kSms) return launch_recurrent<D, BF16, 1>(a, s);
+        if (on_tensor_cores) return launch_chunked<D>(a, s);
+    // a short prompt of few heads: 16 columns per CTA, else 64
+    if (a.nseg == 1 && (int64_t)a.work * (D / 64) < 2 * kSms) return launch_recurrent<D, BF16, 1>(a, s);
     return launch_recurrent<D, BF16, 4>(a, s);
 }
 
@@ -179,7 +204,7 @@ lq_status prefill_rows(const lq_config &c, void *state, const int32_t *slots, in
     a.qk_heads = qk_heads;
     a.group = c.num_heads / qk_heads;
     a.cont = (flags & LQ_PREFILL_CONTINUE) != 0u;
-    Cut cut = cut_of(a.work, tokens);
+    Cut cut = cut_of(c, a.work, tokens);
     if (workspace) {
         if (workspace_size < workspace_bytes(c, a.work, cut)) return LQ_ERR_INVALID_ARG;
     } else {
@@ -195,8 +220,9 @@ lq_status prefill_rows(const lq_config &c, void *state, const int32_t *slots, in
         a.ws_run = a.ws_bad + n;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (c.dk == 128) return c.in_dtype ? launch_prefill<128, true>(a, s) : launch_prefill<128, false>(a, s);
-    return c.in_dtype ? launch_prefill<64, true>(a, s) : launch_prefill<64, false>(a, s);
+    const bool tc = chunked(c, tokens);
+    if (c.dk == 128) return c.in_dtype ? launch_prefill<128, true>(a, tc, s) : launch_prefill<128, false>(a, tc, s);
+    return c.in_dtype ? launch_prefill<64, true>(a, tc, s) : launch_prefill<64, false>(a, tc, s);
 }
 
 lq_status check_linear_slots(const lq_config *cfg, const void *state, const int32_t *slots, int n_active,
@@ -252,7 +278,7 @@ lq_status lq_linear_step_slots(const lq_config *cfg, void *state, const int32_t 
 size_t lq_linear_prefill_workspace(const lq_config *cfg, int rows, int tokens) {
     if (check_linear(cfg, 1) != LQ_OK || rows <= 0 || tokens <= 0) return 0;
     const int64_t work = (int64_t)rows * cfg->num_heads;
-    return workspace_bytes(*cfg, work, cut_of(work, tokens));
+    return workspace_bytes(*cfg, work, cut_of(*cfg, work, tokens));
 }
 
 lq_status lq_linear_prefill(const lq_config *cfg, void *state, int tokens, const int32_t *lengths, const float *S0,

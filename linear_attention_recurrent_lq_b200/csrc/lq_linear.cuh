@@ -181,11 +181,19 @@ __global__ void __launch_bounds__(256, 3) lin_step_kernel(LinArgs A) {
 }
 
 // ------------------------------------------- a prompt, token after token
-// 128 threads hold 16 C columns of one head's state in registers: lane % 8
-// takes the rows 4 (lane % 8) + 32 m .. + 3, lane / 8 and the warp take C
-// columns.  q, k, v and the gates arrive 16 tokens at a time through a ring
-// of three shared-memory stages; rows past the prompt arrive as zeros.  The
-// outputs of eight tokens are summed over the eight row lanes at once.
+// 128 threads hold 64 columns of one head's state in registers (16 where heads
+// are few): lane % 8 takes the rows 4 (lane % 8) + 32 m .. + 3, lane / 8 and the
+// warp take four columns (one).  q, k, v and the gates arrive 16 tokens at a
+// time through a ring of three shared-memory stages; rows past the prompt arrive
+// as zeros.  The outputs of four (eight) tokens are summed over the eight row
+// lanes at once.
+//
+// Bound by FP32 multiply-adds.  The registers hold S / G with G the product of
+// the gates so far, so a token costs two per entry instead of three,
+//     S / G_t += k_t (v_t / G_t),   o_t = G_t (S / G_t)^T q_t,
+// and S is brought back to G = 1 before 16 tokens that start from G < 2^-32.
+// 16 tokens whose gates multiply to less than 2^-60 (gates of 0 among them)
+// are taken one by one from G = 1: S = a_t S + k_t v_t^T.
 constexpr int kLinTokens = 16;  // tokens per stage
 constexpr int kLinStages = 3;
 constexpr int kLinThreads = 128;
@@ -193,6 +201,7 @@ constexpr int kLinThreads = 128;
 template <int D, bool BF16, int C>
 struct LinShape {
     static constexpr int E = BF16 ? 2 : 4;
+    static constexpr int U = C == 1 ? 8 : 4;          // tokens summed at once
     static constexpr int COLS = 16 * C;               // columns of one CTA
     static constexpr int NB = D / COLS;               // CTAs of one head (one cluster)
     static constexpr int QB = D * E, VB = COLS * E;   // bytes of a q / k row, of a v row's columns
@@ -202,11 +211,11 @@ struct LinShape {
 };
 
 template <int D, bool BF16, int C, bool PARTIAL>
-__global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
+__global__ void __launch_bounds__(kLinThreads, 4) lin_recurrent_kernel(LinArgs A) {
     using SH = LinShape<D, BF16, C>;
-    constexpr int E = SH::E, M = D / 32, TB = kLinTokens;
+    constexpr int E = SH::E, RL = 8, U = SH::U, M = D / 32, TB = kLinTokens;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rl = lane & 7, jt = (4 * warp + (lane >> 3)) * C;  // first column inside the CTA
+    const int rl = lane % RL, jt = (32 / RL * warp + lane / RL) * C;  // first column inside the CTA
     const int w = blockIdx.x / SH::NB, jc = (blockIdx.x % SH::NB) * SH::COLS;
     const int seg = blockIdx.y;
     const int row = w / A.map.heads, hh = w - row * A.map.heads;
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
         for (int p = 0; p < 2 * M; ++p)
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int i = 4 * rl + 32 * (p >> 1) + 2 * (p & 1);
+                const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
                 S[p][c] = src ? make_float2(src[(size_t)i * D + jc + jt + c], src[(size_t)(i + 1) * D + jc + jt + c])
                               : make_float2(0.f, 0.f);
             }
@@ -283,7 +292,7 @@ __global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
         cp_async_commit();
     }
 
-    float gprod = 1.f;
+    float G = 1.f, gprod = 1.f;
     int bad = kNoBad, t_done = t_stop;
 #pragma unroll 1
     for (int i = 0; i < n_stage && bad == kNoBad; ++i) {
@@ -307,67 +316,106 @@ __global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
                 *reinterpret_cast<uint4 *>(b + SH::V_OFF + n * SH::VB + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
             __syncthreads();
         }
-#pragma unroll 1
-        for (int g = 0; g < TB && g < n; g += 8) {
-            float p[8][C];
+        // products of the gates: pre up to token lane, all 16 in `total`
+        float pre = al;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const uint8_t *qs = b + (g + u) * SH::QB + 4 * rl * E, *ks = qs + SH::K_OFF;
-                const float a = __shfl_sync(0xFFFFFFFFu, al, g + u);
-                const float2 a2 = make_float2(a, a);
-                if (PARTIAL) gprod *= a;
-                float v[C];
+        for (int d = 1; d < TB; d <<= 1) {
+            const float x = __shfl_up_sync(0xFFFFFFFFu, pre, d, TB);
+            if ((lane & (TB - 1)) >= d) pre *= x;
+        }
+        const float total = __shfl_sync(0xFFFFFFFFu, pre, TB - 1);
+        const bool apart = !(total >= 0x1p-60f);
+        if (apart || G < 0x1p-32f) {
+            const float2 g2 = make_float2(G, G);
 #pragma unroll
-                for (int c = 0; c < C; ++c) v[c] = load_in(b + SH::V_OFF + (g + u) * SH::VB, jt + c, BF16);
-                float2 acc[C];
+            for (int p = 0; p < 2 * M; ++p)
 #pragma unroll
-                for (int c = 0; c < C; ++c) acc[c] = make_float2(0.f, 0.f);
+                for (int c = 0; c < C; ++c) S[p][c] = __fmul2_rn(g2, S[p][c]);
+            G = 1.f;
+        }
+        const float Gl = G * pre, inv = __fdiv_rn(1.f, Gl);  // of token `lane`
+        if (PARTIAL) gprod *= total;
+        if (!apart) G *= total;
+        // S += k v^T of token t, v times f; returns S^T q of this lane's rows
+        auto token = [&](int t, float f, float (&o)[C]) {
+            const uint8_t *qs = b + t * SH::QB + 4 * rl * E, *ks = qs + SH::K_OFF;
+            float v[C];
 #pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const float4 k4 = lin_load4<BF16>(ks + 32 * m * E);
-                    float4 q4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (!PARTIAL) q4 = lin_load4<BF16>(qs + 32 * m * E);
+            for (int c = 0; c < C; ++c) v[c] = f * load_in(b + SH::V_OFF + t * SH::VB, jt + c, BF16);
+            float2 acc[C];
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const float2 v2 = make_float2(v[c], v[c]);
-                        S[2 * m][c] = __ffma2_rn(a2, S[2 * m][c], __fmul2_rn(make_float2(k4.x, k4.y), v2));
-                        S[2 * m + 1][c] = __ffma2_rn(a2, S[2 * m + 1][c], __fmul2_rn(make_float2(k4.z, k4.w), v2));
-                        if (!PARTIAL) {
-                            acc[c] = __ffma2_rn(S[2 * m][c], make_float2(q4.x, q4.y), acc[c]);
-                            acc[c] = __ffma2_rn(S[2 * m + 1][c], make_float2(q4.z, q4.w), acc[c]);
-                        }
-                    }
-                }
+            for (int c = 0; c < C; ++c) acc[c] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int c = 0; c < C; ++c) p[u][c] = acc[c].x + acc[c].y;
-            }
-            if (!PARTIAL && A.out) {
-                // sum over the row lanes; lane rl keeps token g + rl
+            for (int m = 0; m < M; ++m) {
+                const float4 k4 = lin_load4<BF16>(ks + 4 * RL * m * E);
+                float4 q4 = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!PARTIAL) q4 = lin_load4<BF16>(qs + 4 * RL * m * E);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    float r4[4], r2[2];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        r4[x] = ((rl & 4) ? p[4 + x][c] : p[x][c]) +
-                                __shfl_xor_sync(0xFFFFFFFFu, (rl & 4) ? p[x][c] : p[4 + x][c], 4);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        r2[x] = ((rl & 2) ? r4[2 + x] : r4[x]) +
-                                __shfl_xor_sync(0xFFFFFFFFu, (rl & 2) ? r4[x] : r4[2 + x], 2);
-                    p[0][c] = ((rl & 1) ? r2[1] : r2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (rl & 1) ? r2[0] : r2[1], 1);
+                    const float2 v2 = make_float2(v[c], v[c]);
+                    S[2 * m][c] = __ffma2_rn(make_float2(k4.x, k4.y), v2, S[2 * m][c]);
+                    S[2 * m + 1][c] = __ffma2_rn(make_float2(k4.z, k4.w), v2, S[2 * m + 1][c]);
+                    if (!PARTIAL) {
+                        acc[c] = __ffma2_rn(S[2 * m][c], make_float2(q4.x, q4.y), acc[c]);
+                        acc[c] = __ffma2_rn(S[2 * m + 1][c], make_float2(q4.z, q4.w), acc[c]);
+                    }
                 }
-                if (g + rl < n) {
-                    float *o = A.out + lin_v_row(A, row, hh, t0 + g + rl) * D + jc + jt;
-                    if constexpr (C == 4)
-                        *reinterpret_cast<float4 *>(o) = make_float4(p[0][0], p[0][1], p[0][2], p[0][3]);
-                    else
+            }
 #pragma unroll
-                        for (int c = 0; c < C; ++c) o[c] = p[0][c];
+            for (int c = 0; c < C; ++c) o[c] = acc[c].x + acc[c].y;
+        };
+        if (apart) {
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
+                const float a = __shfl_sync(0xFFFFFFFFu, al, t);
+                float o[C];
+#pragma unroll
+                for (int r = 0; r < 2 * M; ++r)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) S[r][c] = __fmul2_rn(make_float2(a, a), S[r][c]);
+                token(t, 1.f, o);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+#pragma unroll
+                    for (int d = RL / 2; d >= 1; d >>= 1) o[c] += __shfl_xor_sync(0xFFFFFFFFu, o[c], d);
+                    if (!PARTIAL && A.out && rl == 0) A.out[lin_v_row(A, row, hh, t0 + t) * D + jc + jt + c] = o[c];
+                }
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int g = 0; g < TB && g < n; g += U) {
+            float p[U][C];
+#pragma unroll
+            for (int u = 0; u < U; ++u) token(g + u, __shfl_sync(0xFFFFFFFFu, inv, g + u), p[u]);
+            if (!PARTIAL && A.out) {
+                // sums over the row lanes; a lane keeps NV columns of one token
+                constexpr int N = U * C, NV = N / RL;
+                float x[N];
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[e] = p[e / C][e % C];
+#pragma unroll
+                for (int d = RL / 2; d >= 1; d >>= 1)
+#pragma unroll
+                    for (int e = 0; e < d * NV; ++e) {
+                        const bool up = (rl & d) != 0;
+                        x[e] = (up ? x[e + d * NV] : x[e]) + __shfl_xor_sync(0xFFFFFFFFu, up ? x[e] : x[e + d * NV], d);
+                    }
+                const int t = g + rl * NV / C;
+                const float go = __shfl_sync(0xFFFFFFFFu, Gl, t);
+                if (t < n) {
+                    float *o = A.out + lin_v_row(A, row, hh, t0 + t) * D + jc + jt + rl * NV % C;
+                    if constexpr (NV == 2) *reinterpret_cast<float2 *>(o) = make_float2(go * x[0], go * x[1]);
+                    else *o = go * x[0];
                 }
             }
         }
     }
     cp_async_wait<0>();
+#pragma unroll
+    for (int p = 0; p < 2 * M; ++p)
+#pragma unroll
+        for (int c = 0; c < C; ++c) S[p][c] = __fmul2_rn(make_float2(G, G), S[p][c]);
 
     if (PARTIAL) {
         float *dst = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D) + jc + jt;
@@ -375,7 +423,7 @@ __global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
         for (int p = 0; p < 2 * M; ++p)
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int i = 4 * rl + 32 * (p >> 1) + 2 * (p & 1);
+                const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
                 dst[(size_t)i * D + c] = S[p][c].x;
                 dst[(size_t)(i + 1) * D + c] = S[p][c].y;
             }
@@ -394,7 +442,7 @@ __global__ void __launch_bounds__(kLinThreads) lin_recurrent_kernel(LinArgs A) {
         for (int p = 0; p < 2 * M; ++p)
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int i = 4 * rl + 32 * (p >> 1) + 2 * (p & 1);
+                const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
                 dst[(size_t)i * D + c] = S[p][c].x;
                 dst[(size_t)(i + 1) * D + c] = S[p][c].y;
             }
