@@ -190,6 +190,28 @@ def _validate(*specs):
             raise ValueError(f"{what}: on cuda:{x.get_device()}, but the library launches on cuda:{dev}")
 
 
+def _addresses(*specs):
+    """The addresses of the specs' tensors, checked as _validate and _ptr do.
+    One pass that a good call needs (2.2 us for six tensors); a bad one goes
+    through the ordered checks for its error."""
+    dtypes = _DTYPES or _dtypes()
+    dev, out = None, []
+    for x, _, dtype, numel, at_least in specs:
+        if x is None or x.__class__ is int:
+            out.append(x)
+            continue
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        n = x.numel()
+        if (x.dtype is not dtypes[dtype] or x.get_device() != dev or not x.is_contiguous()
+                or not (numel is None or n == numel or (at_least and n > numel))):
+            _validate(*specs)
+            return [_ptr(sp[0]) for sp in specs]
+        out.append(x.data_ptr())
+    return out
+
+
 def _spec(x, what, dtype, numel=None, at_least=False):
     return (x, what, dtype, numel, at_least)
 
@@ -381,26 +403,25 @@ def lq_copy_slots(cfg, dst, dst_num_slots, dst_slots, src, src_num_slots, src_sl
 # ---- linear attention with one decay per head ------------------------------
 
 def _linear_specs(cfg, rows, T, qk_heads, q, k, v, decay, out):
-    Hk = cfg.num_heads if qk_heads is None else int(qk_heads)
-    n, m = rows * T * cfg.num_heads, rows * T * Hk
-    return Hk, [_spec(q, "q", _in_dt(cfg), m * cfg.dk), _spec(k, "k", _in_dt(cfg), m * cfg.dk),
-                _spec(v, "v", _in_dt(cfg), n * cfg.dv), _spec(decay, "decay", "f32", n),
-                _spec(out, "out", "f32", n * cfg.dv)]
+    H, d, dt = cfg.num_heads, cfg.dk, "bf16" if cfg.in_dtype else "f32"
+    Hk = H if qk_heads is None else int(qk_heads)
+    n, m = rows * T * H, rows * T * Hk * d
+    return Hk, ((q, "q", dt, m, False), (k, "k", dt, m, False), (v, "v", dt, n * d, False),
+                (decay, "decay", "f32", n, False), (out, "out", "f32", n * d, False))
 
 
 def lq_linear_step(cfg, state, q, k, v, decay, out, qk_heads=None, stream=None):
     """One token: S = a S + k v^T, out = S^T q.  qk_heads: heads of q and k (default: as many as v)."""
     Hk, specs = _linear_specs(cfg, cfg.num_slots, 1, qk_heads, q, k, v, decay, out)
-    _validate(_state_spec(cfg, state), *specs)
-    _check(lib.lq_linear_step(ctypes.byref(cfg), _ptr(state), Hk, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(out),
-                              _stream(stream)), "lq_linear_step")
+    st, *p = _addresses(_state_spec(cfg, state), *specs)
+    _check(lib.lq_linear_step(ctypes.byref(cfg), st, Hk, *p, _stream(stream)), "lq_linear_step")
 
 
 def lq_linear_step_slots(cfg, state, slots, q, k, v, decay, out, qk_heads=None, stream=None):
-    Hk, specs = _linear_specs(cfg, _n(slots), 1, qk_heads, q, k, v, decay, out)
-    _validate(_state_spec(cfg, state), _spec(slots, "slots", "i32"), *specs)
-    _check(lib.lq_linear_step_slots(ctypes.byref(cfg), _ptr(state), _ptr(slots), _n(slots), Hk, _ptr(q), _ptr(k),
-                                    _ptr(v), _ptr(decay), _ptr(out), _stream(stream)), "lq_linear_step_slots")
+    n = _n(slots)
+    Hk, specs = _linear_specs(cfg, n, 1, qk_heads, q, k, v, decay, out)
+    st, sl, *p = _addresses(_state_spec(cfg, state), _spec(slots, "slots", "i32"), *specs)
+    _check(lib.lq_linear_step_slots(ctypes.byref(cfg), st, sl, n, Hk, *p, _stream(stream)), "lq_linear_step_slots")
 
 
 LQ_PREFILL_CONTINUE = 0x1
@@ -419,24 +440,20 @@ def _torch_stream(stream):
     return stream
 
 
-def _linear_workspace(cfg, rows, tokens, workspace, stream):
-    """The workspace of a prefill call: the caller's, or memory of the caching
-    allocator, taken on the call's stream and given back to it, in stream
-    order, when the call has been enqueued (inside a graph capture: memory of
-    that graph's pool)."""
-    need = lq_linear_prefill_workspace(cfg, rows, tokens) if rows > 0 else 0
-    if workspace is not None or not need:
-        return workspace, need
+def _linear_workspace(cfg, rows, tokens, workspace, address, stream):
+    """(tensor to hold, address, bytes) of a prefill call's workspace: the
+    caller's, or memory of the caching allocator, taken on the call's stream and
+    given back to it, in stream order, when the call has been enqueued (inside a
+    graph capture: memory of that graph's pool)."""
+    if workspace is not None and not isinstance(workspace, int):
+        return workspace, address, workspace.numel()
+    need = lq_linear_prefill_workspace(cfg, rows, tokens) if rows > 0 and tokens > 1 else 0
+    if workspace is not None or not need:  # an address's owner vouches for its size
+        return None, workspace, need
     import torch
     with torch.cuda.stream(_torch_stream(stream)):
-        return torch.empty(need, dtype=torch.uint8, device="cuda"), need
-
-
-def _ws_bytes(workspace, need):
-    """Raw addresses are vouched for by their owner."""
-    if workspace is None:
-        return 0
-    return need if isinstance(workspace, int) else workspace.numel()
+        held = torch.empty(need, dtype=torch.uint8, device="cuda")
+    return held, held.data_ptr(), need
 
 
 def lq_linear_prefill(cfg, state, tokens, q, k, v, decay, S0=None, lengths=None, out=None, qk_heads=None,
@@ -446,25 +463,24 @@ def lq_linear_prefill(cfg, state, tokens, q, k, v, decay, S0=None, lengths=None,
     lq_linear_prefill_workspace(cfg, N, T) bytes; allocated here when None."""
     T, rows = max(int(tokens), 0), cfg.num_slots
     Hk, specs = _linear_specs(cfg, rows, T, qk_heads, q, k, v, decay, out)
-    _validate(_state_spec(cfg, state), *specs, _dense_spec(cfg, S0, "S0", rows), _spec(lengths, "lengths", "i32", rows),
-              _spec(workspace, "workspace", "u8"))
-    ws, need = _linear_workspace(cfg, rows, T, workspace, stream)
-    _check(lib.lq_linear_prefill(ctypes.byref(cfg), _ptr(state), int(tokens), _ptr(lengths), _ptr(S0), Hk, _ptr(q),
-                                 _ptr(k), _ptr(v), _ptr(decay), _ptr(out), LQ_PREFILL_CONTINUE if cont else 0,
-                                 _ptr(ws), _ws_bytes(ws, need), _stream(stream)), "lq_linear_prefill")
+    st, *p, s0, ln, ws = _addresses(_state_spec(cfg, state), *specs, _dense_spec(cfg, S0, "S0", rows),
+                                    _spec(lengths, "lengths", "i32", rows), _spec(workspace, "workspace", "u8"))
+    held, ws, size = _linear_workspace(cfg, rows, T, workspace, ws, stream)
+    _check(lib.lq_linear_prefill(ctypes.byref(cfg), st, int(tokens), ln, s0, Hk, *p, LQ_PREFILL_CONTINUE if cont else 0,
+                                 ws, size, _stream(stream)), "lq_linear_prefill")
 
 
 def lq_linear_prefill_slots(cfg, state, slots, tokens, q, k, v, decay, S0=None, lengths=None, out=None,
                             qk_heads=None, cont=False, workspace=None, stream=None):
     T, rows = max(int(tokens), 0), _n(slots)
     Hk, specs = _linear_specs(cfg, rows, T, qk_heads, q, k, v, decay, out)
-    _validate(_state_spec(cfg, state), _spec(slots, "slots", "i32"), *specs, _dense_spec(cfg, S0, "S0", rows),
-              _spec(lengths, "lengths", "i32", rows), _spec(workspace, "workspace", "u8"))
-    ws, need = _linear_workspace(cfg, rows, T, workspace, stream)
-    _check(lib.lq_linear_prefill_slots(ctypes.byref(cfg), _ptr(state), _ptr(slots), rows, int(tokens), _ptr(lengths),
-                                       _ptr(S0), Hk, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(out),
-                                       LQ_PREFILL_CONTINUE if cont else 0, _ptr(ws), _ws_bytes(ws, need),
-                                       _stream(stream)), "lq_linear_prefill_slots")
+    st, sl, *p, s0, ln, ws = _addresses(_state_spec(cfg, state), _spec(slots, "slots", "i32"), *specs,
+                                        _dense_spec(cfg, S0, "S0", rows), _spec(lengths, "lengths", "i32", rows),
+                                        _spec(workspace, "workspace", "u8"))
+    held, ws, size = _linear_workspace(cfg, rows, T, workspace, ws, stream)
+    _check(lib.lq_linear_prefill_slots(ctypes.byref(cfg), st, sl, rows, int(tokens), ln, s0, Hk, *p,
+                                       LQ_PREFILL_CONTINUE if cont else 0, ws, size, _stream(stream)),
+           "lq_linear_prefill_slots")
 
 
 # ---- norms and gates around the recurrence ---------------------------------
@@ -490,12 +506,13 @@ def lq_qk_norm(cfg, q, k, a, b, a_log, dt_bias, q_out, k_out, decay, beta, q_sca
     Hk = H if qk_heads is None else int(qk_heads)
     M = _rows(q, Hk * cfg.dk, "q", rows)
     n, ch, dt = M * H, (cfg.dk if cfg.decay_kind == 1 else 1), _in_dt(cfg)
-    _validate(*[_spec(x, w, dt, M * Hk * cfg.dk) for x, w in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))],
-              _spec(a, "a", dt, n * ch), _spec(b, "b", dt, n), _spec(a_log, "a_log", "f32", H),
-              _spec(dt_bias, "dt_bias", "f32", H * ch), _spec(decay, "decay", "f32", n * ch), _spec(beta, "beta", "f32", n))
-    _check(lib.lq_qk_norm(ctypes.byref(cfg), M, Hk, _ptr(q), _ptr(k), _ptr(a), _ptr(b), _ptr(a_log), _ptr(dt_bias),
-                          float(q_scale), float(eps), _ptr(q_out), _ptr(k_out), _ptr(decay), _ptr(beta),
-                          _stream(stream)), "lq_qk_norm")
+    m = M * Hk * cfg.dk
+    p = _addresses((q, "q", dt, m, False), (k, "k", dt, m, False), (a, "a", dt, n * ch, False), (b, "b", dt, n, False),
+                   (a_log, "a_log", "f32", H, False), (dt_bias, "dt_bias", "f32", H * ch, False),
+                   (q_out, "q_out", dt, m, False), (k_out, "k_out", dt, m, False), (decay, "decay", "f32", n * ch, False),
+                   (beta, "beta", "f32", n, False))
+    _check(lib.lq_qk_norm(ctypes.byref(cfg), M, Hk, *p[:6], float(q_scale), float(eps), *p[6:], _stream(stream)),
+           "lq_qk_norm")
 
 
 def lq_out_norm(cfg, o, y, weight=None, gate=None, gate_kind="none", eps=1e-6, rows=None, stream=None):
@@ -504,10 +521,10 @@ def lq_out_norm(cfg, o, y, weight=None, gate=None, gate_kind="none", eps=1e-6, r
         raise ValueError(f"gate_kind {gate_kind!r}, expected one of {', '.join(GATE_KINDS)}")
     M = _rows(o, cfg.num_heads * cfg.dv, "o", rows)
     n = M * cfg.num_heads * cfg.dv
-    _validate(_spec(o, "o", "f32", n), _spec(y, "y", _in_dt(cfg), n), _spec(weight, "weight", "f32", cfg.dv),
-              _spec(gate, "gate", _in_dt(cfg), n))
-    _check(lib.lq_out_norm(ctypes.byref(cfg), M, _ptr(o), _ptr(weight), _ptr(gate), GATE_KINDS[gate_kind], float(eps),
-                           _ptr(y), _stream(stream)), "lq_out_norm")
+    po, py, pw, pg = _addresses(_spec(o, "o", "f32", n), _spec(y, "y", _in_dt(cfg), n),
+                                _spec(weight, "weight", "f32", cfg.dv), _spec(gate, "gate", _in_dt(cfg), n))
+    _check(lib.lq_out_norm(ctypes.byref(cfg), M, po, pw, pg, GATE_KINDS[gate_kind], float(eps), py, _stream(stream)),
+           "lq_out_norm")
 
 
 def lq_selftest_wait(status, stream=None):

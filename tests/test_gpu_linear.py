@@ -89,7 +89,7 @@ def run_prefill(st, x, S0=None, lengths=None, cont=False, cut=True, out=True, sl
     call = dict(state=st.buf, tokens=t, q=x["q"], k=x["k"], v=x["v"], decay=x["decay"])
     if not cut:  # a null workspace reaches the library as it is
         real = b._linear_workspace
-        b._linear_workspace = lambda *a: (None, 0)
+        b._linear_workspace = lambda *a: (None, None, 0)
     try:
         if slots is None:
             b.lq_linear_prefill(st.cfg, **call, **args)
