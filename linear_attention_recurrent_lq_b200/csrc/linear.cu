@@ -35,13 +35,14 @@ Cut cut_of(const lq_config &c, int64_t work, int tokens) {
     Cut best{tokens > 0 ? tokens : 1, 1};
     if (work <= 0 || tokens < 256) return best;
     if (chunked(c, tokens)) {
-        // One CTA per SM and kind of pass; time of a chunk of 64 tokens in the
-        // main pass, in the first pass, and of the launches and the scan, in
-        // units of 0.1 us as measured at d = 128
-        const int64_t main = 27, first = 12, fixed = 150;
+        // One CTA per SM and kind of pass.  In units of 0.1 us, as measured at
+        // d = 128: 27 for a chunk of 64 tokens in the main pass and 12 in the
+        // first, 15 and 30 for each segment's start, 0.3 a segment in the scan,
+        // 60 for the launches.  32 heads of 16384 tokens: 230 us in 9 segments
+        // (this choice), 275 us in 32.
         auto cost = [&](int64_t n, int64_t chunks) {
-            const int64_t t = (work * n + kSms - 1) / kSms * chunks * main;
-            return n == 1 ? t : t + (work * (n - 1) + kSms - 1) / kSms * chunks * first + fixed;
+            const int64_t t = (work * n + kSms - 1) / kSms * (chunks * 27 + 15);
+            return n == 1 ? t : t + (work * (n - 1) + kSms - 1) / kSms * (chunks * 12 + 30) + work * n * 3 / 10 + 60;
         };
         const int64_t all = (tokens + 63) / 64;
         int64_t least = cost(1, all);

@@ -92,8 +92,8 @@ __device__ __forceinline__ int claimed_cta(uint32_t answer) {  // -1: none is le
     return got ? (int)x : -1;
 }
 
-__device__ __forceinline__ void lin_give_up(const LinArgs &A, int it) {
-    const int w = it / A.nseg, bi = w >= 0 && w < A.work ? A.map.blob(w) : -1;
+__device__ __forceinline__ void lin_give_up(const LinArgs &A, int w) {
+    const int bi = w >= 0 && w < A.work ? A.map.blob(w) : -1;
     if (bi >= 0) set_status(A.state + (size_t)bi * A.L.blob, LQ_DEV_TIMEOUT);
 }
 
@@ -162,6 +162,21 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             if (r >= kLpRing) wait(&bars->ring_free[r % kLpRing], r / kLpRing - 1u);
             return ring + r % kLpRing;
         };
+        // Up to 32 rows of given lengths are taken longest first, so that the last
+        // items to start are short: lane r finds the row of rank r.
+        const int rows = A.work / A.map.heads;
+        const bool ranked = A.lengths != nullptr && rows <= 32;
+        int row_of_rank = lane;
+        if (ranked) {
+            const int mine = lane < rows ? lin_length(A, lane) : -1;
+            int rank = 0;
+            for (int i = 0; i < 32; ++i) {
+                const int other = __shfl_sync(0xFFFFFFFFu, mine, i);
+                rank += other > mine || (other == mine && i < lane);
+            }
+            for (int i = 0; i < 32; ++i)
+                if (__shfl_sync(0xFFFFFFFFu, rank, i) == lane) row_of_rank = i;
+        }
 #pragma unroll 1
         for (int it = blockIdx.x, next = it; it >= 0 && ok; it = next) {
             // the next item, while this one is fed
@@ -172,8 +187,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 fence_async_smem();  // the answer has been read before the next one is written
                 __syncwarp();
             };
-            const int w = it / A.nseg, seg = it - w * A.nseg;
-            const int row = w / A.map.heads, hh = w - row * A.map.heads;
+            int w = it / A.nseg;
+            const int seg = it - w * A.nseg, hh = w % A.map.heads;
+            int row = w / A.map.heads;
+            if (ranked) row = __shfl_sync(0xFFFFFFFFu, row_of_rank, row);
+            w = row * A.map.heads + hh;
             const int len = lin_length(A, row), last = lin_last_segment(A, len);
             const int bi = A.map.blob(w);
             uint8_t *blob = A.state + (size_t)(bi < 0 ? 0 : bi) * A.L.blob;
@@ -271,9 +289,13 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 }
             }
             claimed();
-            if (!ok && lane == 0) {  // claimed, but not to be done
-                lin_give_up(A, it);
-                if (next >= 0) lin_give_up(A, next);
+            if (!ok) {  // claimed, but not to be done
+                int nw = next >= 0 && next < A.work * A.nseg ? next / A.nseg : w;
+                if (ranked) nw = __shfl_sync(0xFFFFFFFFu, row_of_rank, nw / A.map.heads) * A.map.heads + nw % A.map.heads;
+                if (lane == 0) {
+                    lin_give_up(A, w);
+                    lin_give_up(A, nw);
+                }
             }
         }
         LpSlot *sl = slot_wait();
@@ -626,9 +648,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             arrive(&bars->ring_free[r % kLpRing]);
         }
         if (!ok && lane == 0) {  // the items that are described may not be done
-            lin_give_up(A, w * A.nseg);
+            lin_give_up(A, w);
             for (int i = 0; i < kLpRing; ++i)
-                if (!(ring[i].flags & kLpEnd)) lin_give_up(A, ring[i].w * A.nseg);
+                if (!(ring[i].flags & kLpEnd)) lin_give_up(A, ring[i].w);
         }
     }
     tc_fence_before();
