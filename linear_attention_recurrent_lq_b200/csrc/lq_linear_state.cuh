@@ -161,8 +161,11 @@ __global__ void __launch_bounds__(kLsThreads, 1)
 #pragma unroll 1
         for (int i = warp / (kLsKeys / 2); i < chunks && ok; i += 2) {
             const uint32_t st = (uint32_t)i % kLsStages;
-            wait(&bars->full[st], (uint32_t)i / kLsStages);
+            // in this order: the products of chunk i - 2 stand behind those of
+            // chunk i - 3, so the stage's phase before this one has ended for the
+            // group that did not wait for it, too
             if (i >= 2) wait(&bars->d_done[i & 1], (uint32_t)i / 2u - 1u);
+            wait(&bars->full[st], (uint32_t)i / kLsStages);
             const float *W = reinterpret_cast<const float *>(smem + SH::W + st * 256u);
 #pragma unroll 2
             for (int x = tid % (kLsKeys * 16); x < C * NP; x += kLsKeys * 16) {
