@@ -17,10 +17,19 @@ namespace {
 
 constexpr int kSms = 148;
 
-// bf16 prompts from here on take the chunkwise form on the tensor cores
-constexpr int kMinChunked = 32;
-
-bool chunked(const lq_config &c, int tokens) { return c.in_dtype == 1 && tokens >= kMinChunked; }
+// Whether a bf16 prompt takes the chunkwise form on the tensor cores.  It costs
+// a chunk of 64 tokens whatever the prompt's length; token after token the time
+// grows with the tokens, but few heads spread over more SMs.  Measured, d = 128:
+// 12 heads, 48 tokens 15.2 us chunkwise and 13.2 us token after token, 64 tokens
+// 15.2 and 13.2; 48 heads, 64 tokens 12.3 and 18.4; 128 heads, 4 tokens 15.4 and
+// 19.4.  d = 64: 12 heads, 64 tokens
+// 11.2 and 12.3; 256 heads, 16 tokens 17.4 and 17.4; 2048 heads, 32 tokens 66.6
+// and 60.3, 48 tokens 66.6 and 76.8.
+bool chunked(const lq_config &c, int64_t work, int tokens) {
+    if (c.in_dtype != 1) return false;
+    if (work * (c.dk / 16) <= kSms) return tokens >= 65;  // a CTA of 16 columns for each SM
+    return tokens >= (c.dk == 128 && work >= kSms / 2 ? 4 : 33);
+}
 
 // Where the heads alone leave SMs idle, a prompt is cut along time into `nseg`
 // segments of `seg_len` tokens.  That costs a pass over k and v for what the
@@ -34,7 +43,7 @@ struct Cut {
 Cut cut_of(const lq_config &c, int64_t work, int tokens) {
     Cut best{tokens > 0 ? tokens : 1, 1};
     if (work <= 0 || tokens < 256) return best;
-    if (chunked(c, tokens)) {
+    if (chunked(c, work, tokens)) {
         // One CTA per SM and kind of pass.  In units of 0.1 us, as measured at
         // d = 128: 27 for a chunk of 64 tokens in the main pass and 12 in the
         // first, 15 and 30 for each segment's start, 0.3 a segment in the scan,
@@ -221,7 +230,7 @@ lq_status prefill_rows(const lq_config &c, void *state, const int32_t *slots, in
         a.ws_run = a.ws_bad + n;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool tc = chunked(c, tokens);
+    const bool tc = chunked(c, a.work, tokens);
     if (c.dk == 128) return c.in_dtype ? launch_prefill<128, true>(a, tc, s) : launch_prefill<128, false>(a, tc, s);
     return c.in_dtype ? launch_prefill<64, true>(a, tc, s) : launch_prefill<64, false>(a, tc, s);
 }

@@ -197,6 +197,7 @@ def test_prefill_lengths_of_a_prompt(t, d, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,h,hk,d,t", [(40, 12, 4, 128, 70), (80, 12, 12, 64, 100), (300, 1, 1, 128, 65), (1, 1, 1, 64, 200),
+                                        (40, 12, 4, 128, 5), (100, 1, 1, 128, 17), (90, 2, 1, 64, 33),
                                         (5, 36, 12, 128, 130)])
 def test_prefill_head_layouts(n, h, hk, d, t, dtype):
     x = inputs(6, n, t, h, hk, d, DT[dtype])
