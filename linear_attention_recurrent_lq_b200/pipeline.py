@@ -12,6 +12,12 @@ copy engines.  Buffers are reused from step to step, ordered by events: an
 upload waits for the previous step's window to be done with that layer's
 input buffers, a window for the previous step's download of its output
 buffer.
+
+A layer with `Projections` takes the raw projections instead (q, k, v, the decay
+logits a, the write-strength logits b and, with an output gate, gate): its
+window starts with lq_qk_norm over all W tokens and ends with lq_out_norm, so
+that normalised keys and gates never cross the host link and the rows that come
+back are in the input type, half the bytes of the FP32 rows with bf16.
 """
 from __future__ import annotations
 
@@ -21,13 +27,29 @@ NAMES = ("q", "k", "v", "beta", "decay")
 
 
 @dataclass
+class Projections:
+    """What turns a layer's raw projections into the recurrence's inputs, and
+    its FP32 rows into the layer's: parameters of lq_qk_norm and lq_out_norm
+    (device tensors a_log [H], dt_bias [H] or [H, dk], weight [dv] or None)."""
+    a_log: object
+    dt_bias: object
+    weight: object = None
+    gate_kind: str = "silu"
+    q_scale: float = 1.0
+    eps: float = 1e-6
+    linear: bool = False   # plain decayed heads (lq_linear_step) instead of the delta rule
+
+
+@dataclass
 class Layer:
     state: object          # an LQState
-    dev_in: dict           # name -> device tensor [W, ...]
-    dev_out: object        # device tensor [W, rows, H, dv]
+    dev_in: dict           # name -> device tensor [W, ...]: q, k, v, beta, decay; with proj q, k, v, a, b (, gate)
+    dev_out: object        # device tensor [W, rows, H, dv]: FP32 rows; with proj in the input type
     host_in: dict          # name -> pinned host tensor, same shapes
     host_out: object       # pinned host tensor, same shape as dev_out
     graph: object = field(default=None)
+    proj: object = field(default=None)   # Projections, or None
+    scratch: dict = field(default=None)  # with proj: normalised q and k, gates, FP32 rows
 
 
 class HostIOPipeline:
@@ -37,6 +59,15 @@ class HostIOPipeline:
         self.layers = layers
         self.window = window
         self.flush = flush
+        for lay in layers:
+            if lay.proj is not None:
+                x, c = lay.dev_in, lay.state.cfg
+                heads = (*x["v"].shape[:-1],)  # [W, rows, H]
+                f32 = dict(dtype=torch.float32, device=x["v"].device)
+                lay.scratch = dict(q=torch.empty_like(x["q"]), k=torch.empty_like(x["k"]), v=x["v"],
+                                   beta=torch.empty(heads, **f32),
+                                   decay=torch.empty(heads + ((c.dk,) if c.decay_kind == 1 else ()), **f32),
+                                   rows=torch.empty(x["v"].shape, **f32))
         self.up = torch.cuda.Stream()
         self.comp = torch.cuda.Stream()
         self.down = torch.cuda.Stream()
@@ -46,11 +77,24 @@ class HostIOPipeline:
         self.down_done = [torch.cuda.Event() for _ in range(n)]
 
     def _window(self, lay: Layer):
-        x = lay.dev_in
+        x, p, rows = lay.dev_in, lay.proj, lay.dev_out
+        if p is not None:
+            from . import binding as B
+            s, rows = lay.scratch, lay.scratch["rows"]
+            hk = x["q"].shape[-2]
+            B.lq_qk_norm(lay.state.cfg, x["q"], x["k"], x["a"], x["b"], p.a_log, p.dt_bias, s["q"], s["k"], s["decay"],
+                         s["beta"], q_scale=p.q_scale, eps=p.eps, qk_heads=hk)
+            raw, x = x, s
         for t in range(self.window):
-            lay.state.step(x["q"][t], x["k"][t], x["v"][t], x["beta"][t], x["decay"][t], lay.dev_out[t])
+            if p is not None and p.linear:
+                lay.state.linear_step(x["q"][t], x["k"][t], x["v"][t], x["decay"][t], rows[t], qk_heads=hk)
+            else:
+                lay.state.step(x["q"][t], x["k"][t], x["v"][t], x["beta"][t], x["decay"][t], rows[t])
         if self.flush:
             lay.state.flush()
+        if p is not None:
+            B.lq_out_norm(lay.state.cfg, rows, lay.dev_out, weight=p.weight, gate=raw.get("gate"),
+                          gate_kind=p.gate_kind, eps=p.eps)
 
     def capture(self):
         """One graph per layer (run once eagerly first, which also sets the
@@ -78,7 +122,7 @@ class HostIOPipeline:
         for i, lay in enumerate(self.layers):
             with torch.cuda.stream(self.up):
                 self.up.wait_event(self.comp_done[i])
-                for name in NAMES:
+                for name in NAMES if lay.proj is None else lay.host_in:
                     lay.dev_in[name].copy_(lay.host_in[name], non_blocking=True)
                 self.up_done[i].record(self.up)
             with torch.cuda.stream(self.comp):

@@ -443,3 +443,42 @@ def test_the_same_inputs_give_the_same_bits(n, h, d, t):
         for _ in range(10):
             st.linear_prefill(t, x["q"], x["k"], x["v"], x["decay"], S0=x["S0"], out=again)
         assert torch.equal(again, o) and torch.equal(st.buf, state)
+
+
+def test_offsets_beyond_32_bits():
+    """A state buffer of more than 2^32 bytes, and a prompt whose outputs have
+    more than 2^31 elements: the last head and the last tokens are right."""
+    b = B()
+    n, h, d = 1100, 60, 128
+    st = state_of(n, h, d, torch.bfloat16)
+    assert st.buf.numel() > 2 ** 32
+    st.buf.zero_()
+    blobs = st.blobs()
+    blobs[:, 12:16].view(torch.int32)[:] = 0x4C515354
+    S0 = torch.randn(d, d, device="cuda")
+    blobs[-1, 128:128 + 4 * d * d].view(torch.float32).view(d, d).copy_(S0)
+    x = inputs(60, n, 1, h, 1, d, torch.bfloat16)["q"]
+    y = inputs(61, n, 1, 1, 1, d, torch.bfloat16)
+    v = y["v"].expand(n, 1, h, d).contiguous()
+    a = torch.full((n, h), 0.5, device="cuda")
+    out = torch.empty(n, h, d, device="cuda")
+    st.linear_step(x[:, 0].contiguous(), y["k"][:, 0].contiguous(), v[:, 0].contiguous(), a, out, qk_heads=1)
+    S = 0.5 * S0.double() + torch.outer(y["k"][-1, 0, 0].double(), v[-1, 0, -1].double())
+    near(blobs[-1, 128:128 + 4 * d * d].view(torch.float32).view(d, d), S, "last state")
+    near(out[-1, -1], S.T @ x[-1, 0, 0].double(), "last output")
+    del st, blobs, v, out, S
+    torch.cuda.empty_cache()
+    h, t, tail = 16, 2 ** 31 // (16 * 128) + 1000, 7
+    x = inputs(62, 1, t, 1, 1, d, torch.bfloat16)
+    v = torch.randn(1, t, h, d, device="cuda", dtype=torch.bfloat16)
+    a = torch.rand(1, t, h, device="cuda")
+    a[:, t - tail] = 0
+    out = torch.empty(1, t, h, d, device="cuda")
+    assert out.numel() > 2 ** 31
+    st = state_of(1, h, d, torch.bfloat16)
+    st.linear_prefill(t, x["q"], x["k"], v, a, out=out, qk_heads=1)
+    end = dict(q=x["q"][:, -tail:], k=x["k"][:, -tail:], v=v[:, -tail:], decay=a[:, -tail:])
+    want, S = reference(end, None)
+    near(out[:, -tail:], want, "last tokens")
+    near(st.dequant(), S, "last state")
+    assert st.check() == b.LQ_OK
