@@ -210,6 +210,25 @@ struct LinShape {
     static constexpr uint32_t SMEM = (uint32_t)(kLinStages * STAGE);
 };
 
+// C columns of one state row (null: zeros).
+template <int C>
+__device__ __forceinline__ void lin_get_row(const float *p, float (&x)[C]) {
+    if constexpr (C == 4) {
+        const float4 v = p ? *reinterpret_cast<const float4 *>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = p ? p[c] : 0.f;
+    }
+}
+template <int C>
+__device__ __forceinline__ void lin_put_row(float *p, const float (&x)[C]) {
+    if constexpr (C == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+#pragma unroll
+        for (int c = 0; c < C; ++c) p[c] = x[c];
+}
+
 template <int D, bool BF16, int C, bool PARTIAL>
 __global__ void __launch_bounds__(kLinThreads, 4) lin_recurrent_kernel(LinArgs A) {
     using SH = LinShape<D, BF16, C>;
@@ -251,13 +270,14 @@ __global__ void __launch_bounds__(kLinThreads, 4) lin_recurrent_kernel(LinArgs A
         const float *src = nullptr;
         if (!PARTIAL && run && seg <= last) src = lin_state_source(A, w, seg, blob);
 #pragma unroll
-        for (int p = 0; p < 2 * M; ++p)
+        for (int p = 0; p < 2 * M; ++p) {
+            float a[C], b[C];
+            const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
+            lin_get_row<C>(src ? src + (size_t)i * D + jc + jt : nullptr, a);
+            lin_get_row<C>(src ? src + (size_t)(i + 1) * D + jc + jt : nullptr, b);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
-                S[p][c] = src ? make_float2(src[(size_t)i * D + jc + jt + c], src[(size_t)(i + 1) * D + jc + jt + c])
-                              : make_float2(0.f, 0.f);
-            }
+            for (int c = 0; c < C; ++c) S[p][c] = make_float2(a[c], b[c]);
+        }
     }
 
     const uint8_t *qg = static_cast<const uint8_t *>(A.q), *kg = static_cast<const uint8_t *>(A.k);
@@ -420,13 +440,17 @@ __global__ void __launch_bounds__(kLinThreads, 4) lin_recurrent_kernel(LinArgs A
     if (PARTIAL) {
         float *dst = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D) + jc + jt;
 #pragma unroll
-        for (int p = 0; p < 2 * M; ++p)
+        for (int p = 0; p < 2 * M; ++p) {
+            float a[C], b[C];
+            const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
-                dst[(size_t)i * D + c] = S[p][c].x;
-                dst[(size_t)(i + 1) * D + c] = S[p][c].y;
+                a[c] = S[p][c].x;
+                b[c] = S[p][c].y;
             }
+            lin_put_row<C>(dst + (size_t)i * D, a);
+            lin_put_row<C>(dst + (size_t)(i + 1) * D, b);
+        }
         if (tid == 0 && jc == 0) {
             A.ws_g[(size_t)w * A.nseg + seg] = gprod;
             A.ws_bad[(size_t)w * A.nseg + seg] = bad;
@@ -439,13 +463,17 @@ __global__ void __launch_bounds__(kLinThreads, 4) lin_recurrent_kernel(LinArgs A
     if (run && (bad != kNoBad || seg == last)) {  // this segment holds the prompt's end
         float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + jc + jt;
 #pragma unroll
-        for (int p = 0; p < 2 * M; ++p)
+        for (int p = 0; p < 2 * M; ++p) {
+            float a[C], b[C];
+            const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int i = 4 * rl + 4 * RL * (p >> 1) + 2 * (p & 1);
-                dst[(size_t)i * D + c] = S[p][c].x;
-                dst[(size_t)(i + 1) * D + c] = S[p][c].y;
+                a[c] = S[p][c].x;
+                b[c] = S[p][c].y;
             }
+            lin_put_row<C>(dst + (size_t)i * D, a);
+            lin_put_row<C>(dst + (size_t)(i + 1) * D, b);
+        }
         if (tid == 0 && jc == 0) lin_write_header(blob, A.cont, bad != kNoBad);
     }
 }
@@ -476,9 +504,9 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs A) {
     const int last = lin_last_segment(A, lin_length(A, row));
     float *S = A.ws_S + (size_t)w * A.nseg * (D * D) + e;
     const float *g = A.ws_g + (size_t)w * A.nseg;
-    // eight segments' loads in flight (one at a time: 30 us for 32 heads of 9
+    // sixteen segments' loads in flight (one at a time: 30 us for 32 heads of 9
     // segments, d = 128)
-    constexpr int U = 8;
+    constexpr int U = 16;
 #pragma unroll 1
     for (int s0 = 0; s0 < last; s0 += U) {
         float4 own[U];
