@@ -188,6 +188,8 @@ lq_status launch_prefill(const LinArgs &a, bool on_tensor_cores, cudaStream_t s)
         if (on_tensor_cores) return launch_chunked<D>(a, s);
     // a short prompt of few heads: 16 columns per CTA, else 64
     if (a.nseg == 1 && (int64_t)a.work * (D / 64) < 2 * kSms) return launch_recurrent<D, BF16, 1>(a, s);
+    if constexpr (D == 128)
+        if (a.work >= 2 * kSms) return launch_recurrent<D, BF16, 8>(a, s);
     return launch_recurrent<D, BF16, 4>(a, s);
 }
 

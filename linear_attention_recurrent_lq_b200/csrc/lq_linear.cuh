@@ -201,7 +201,7 @@ constexpr int kLinThreads = 128;
 template <int D, bool BF16, int C>
 struct LinShape {
     static constexpr int E = BF16 ? 2 : 4;
-    static constexpr int U = C == 1 ? 8 : 4;          // tokens summed at once
+    static constexpr int U = C == 1 ? 8 : C == 4 ? 4 : 2;          // tokens summed at once
     static constexpr int COLS = 16 * C;               // columns of one CTA
     static constexpr int NB = D / COLS;               // CTAs of one head (one cluster)
     static constexpr int QB = D * E, VB = COLS * E;   // bytes of a q / k row, of a v row's columns
@@ -213,9 +213,12 @@ struct LinShape {
 // C columns of one state row (null: zeros).
 template <int C>
 __device__ __forceinline__ void lin_get_row(const float *p, float (&x)[C]) {
-    if constexpr (C == 4) {
-        const float4 v = p ? *reinterpret_cast<const float4 *>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    if constexpr (C % 4 == 0) {
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+            const float4 v = p ? *reinterpret_cast<const float4 *>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[c] = v.x; x[c + 1] = v.y; x[c + 2] = v.z; x[c + 3] = v.w;
+        }
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) x[c] = p ? p[c] : 0.f;
@@ -223,14 +226,17 @@ __device__ __forceinline__ void lin_get_row(const float *p, float (&x)[C]) {
 }
 template <int C>
 __device__ __forceinline__ void lin_put_row(float *p, const float (&x)[C]) {
-    if constexpr (C == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    else
+    if constexpr (C % 4 == 0) {
+#pragma unroll
+        for (int c = 0; c < C; c += 4) *reinterpret_cast<float4 *>(p + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+    } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) p[c] = x[c];
+    }
 }
 
 template <int D, bool BF16, int C, bool PARTIAL>
-__global__ void __launch_bounds__(kLinThreads, 4) lin_recurrent_kernel(LinArgs A) {
+__global__ void __launch_bounds__(kLinThreads, C == 8 ? 2 : 4) lin_recurrent_kernel(LinArgs A) {
     using SH = LinShape<D, BF16, C>;
     constexpr int E = SH::E, RL = 8, U = SH::U, M = D / 32, TB = kLinTokens;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
