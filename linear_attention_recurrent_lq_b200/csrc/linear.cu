@@ -31,6 +31,14 @@ bool chunked(const lq_config &c, int64_t work, int tokens) {
     return tokens >= (c.dk == 128 && work >= kSms / 2 ? 4 : 33);
 }
 
+// Token after token with d = 128: whether a CTA takes all 128 columns (eight per
+// lane, so that shared memory is read half as often) and not 64.  f32, 2048
+// heads of 256 tokens: 831 us and 962 us; 16 heads of 8192 tokens, cut along
+// time: 342 and 400; 3 heads of 300 tokens: 31 and 22.
+bool wide(const lq_config &c, int64_t work, int tokens) {
+    return c.dv == 128 && (work >= 2 * kSms || tokens >= 512);
+}
+
 // Where the heads alone leave SMs idle, a prompt is cut along time into `nseg`
 // segments of `seg_len` tokens.  That costs a pass over k and v for what the
 // segments leave behind, and a scan over those states.
@@ -64,12 +72,11 @@ Cut cut_of(const lq_config &c, int64_t work, int tokens) {
         }
         return best;
     }
-    // Token after token: CTAs of 64 columns, six per SM (three with d = 128, whose
-    // CTAs do twice the work), segments of 32 tokens or more.  f32, d = 64, 36
-    // heads of 777 tokens: 36 us so, 44 us with three per SM and 64 tokens; d =
-    // 128, 8 heads of 4096 tokens: 114 us, 124 us with six per SM
-    const int64_t ctas = work * (c.dv / 64);
-    int64_t n = (c.dv == 64 ? 6 : 3) * kSms / ctas;
+    // Token after token: six CTAs (of 64 columns) per SM, with d = 128 three, or
+    // two of 128 columns; segments of 32 tokens or more.  f32, d = 64, 36 heads
+    // of 777 tokens: 36 us so, 44 us with three per SM and 64 tokens
+    const int64_t per_sm = c.dv == 64 ? 6 : wide(c, work, tokens) ? 2 : 3, ctas = work * (per_sm == 3 ? 2 : 1);
+    int64_t n = per_sm * kSms / ctas;
     if (n > tokens / 32) n = tokens / 32;
     if (n > kMaxSegments) n = kMaxSegments;
     if (n < 2) return best;
@@ -183,13 +190,13 @@ lq_status launch_chunked(const LinArgs &a, cudaStream_t s) {
 }
 
 template <int D, bool BF16>
-lq_status launch_prefill(const LinArgs &a, bool on_tensor_cores, cudaStream_t s) {
+lq_status launch_prefill(const lq_config &c, const LinArgs &a, cudaStream_t s) {
     if constexpr (BF16)
-        if (on_tensor_cores) return launch_chunked<D>(a, s);
-    // a short prompt of few heads: 16 columns per CTA, else 64
+        if (chunked(c, a.work, a.tokens)) return launch_chunked<D>(a, s);
+    // a short prompt of few heads: 16 columns per CTA
     if (a.nseg == 1 && (int64_t)a.work * (D / 64) < 2 * kSms) return launch_recurrent<D, BF16, 1>(a, s);
     if constexpr (D == 128)
-        if (a.work >= 2 * kSms) return launch_recurrent<D, BF16, 8>(a, s);
+        if (wide(c, a.work, a.tokens)) return launch_recurrent<D, BF16, 8>(a, s);
     return launch_recurrent<D, BF16, 4>(a, s);
 }
 
@@ -234,9 +241,8 @@ lq_status prefill_rows(const lq_config &c, void *state, const int32_t *slots, in
         a.ws_run = a.ws_bad + n;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool tc = chunked(c, a.work, tokens);
-    if (c.dk == 128) return c.in_dtype ? launch_prefill<128, true>(a, tc, s) : launch_prefill<128, false>(a, tc, s);
-    return c.in_dtype ? launch_prefill<64, true>(a, tc, s) : launch_prefill<64, false>(a, tc, s);
+    if (c.dk == 128) return c.in_dtype ? launch_prefill<128, true>(c, a, s) : launch_prefill<128, false>(c, a, s);
+    return c.in_dtype ? launch_prefill<64, true>(c, a, s) : launch_prefill<64, false>(c, a, s);
 }
 
 lq_status check_linear_slots(const lq_config *cfg, const void *state, const int32_t *slots, int n_active,
