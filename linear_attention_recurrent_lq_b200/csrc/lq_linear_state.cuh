@@ -12,7 +12,7 @@
 // One CTA takes one (head, segment): two groups of eight warps weight the keys
 // of even and of odd chunks (one after the other, all sixteen: 2400 clocks per
 // chunk, the latency of that work), one thread issues the products, one warp
-// feeds (gates, TMA).  Bound by HBM: 516 bytes per token and head (d = 128),
+// loads (TMA), one makes the weights from the gates.  Bound by HBM: 516 bytes per token and head (d = 128),
 // 1390 clocks per chunk and SM; 768 are tensor time.
 #pragma once
 
@@ -21,7 +21,7 @@
 namespace lq {
 
 constexpr int kLsKeys = 16;  // warps that weight the keys
-constexpr int kLsThreads = (kLsKeys + 2) * 32;
+constexpr int kLsThreads = (kLsKeys + 3) * 32;
 constexpr int kLsStages = 3;
 constexpr int kLsGates = 8;  // chunks of gates on their way (a gate is a memory latency of its own)
 
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     const uint32_t base = smem_u32(smem);
     if (tid == 0) {
         for (int i = 0; i < kLsStages; ++i) {
-            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->full[i], 2);  // the loads, and the weights
             mbar_init(&bars->empty[i], 1);
         }
         mbar_init(&bars->all_done, 1);
@@ -79,10 +79,27 @@ __global__ void __launch_bounds__(kLsThreads, 1)
         if (!mbar_try_wait(b, phase & 1u) && !mbar_wait_bounded(b, phase & 1u)) ok = false;
     };
 
-    if (warp == kLsKeys + 1) {  // the feeder
+    if (warp == kLsKeys + 2) {  // the loads
+        const int x = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens + t_begin;
+#pragma unroll 1
+        for (int i = 0; i < chunks && ok; ++i) {
+            const uint32_t st = (uint32_t)i % kLsStages;
+            if (i >= kLsStages) wait(&bars->empty[st], (uint32_t)i / kLsStages - 1u);
+            if (ok && lc_elect()) {
+                uint8_t *sp = smem + st * SH::STAGE;
+                const int y = y0 + (chunks - 1 - i) * C;
+                mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    tma_load_2d(sp + kb * 8192, &mk, x + 64 * kb, y, &bars->full[st]);
+                    tma_load_2d(sp + SH::V + kb * 8192, &mv, xv + 64 * kb, y, &bars->full[st]);
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp == kLsKeys + 1) {  // the weights
         const float *gates = A.decay + lin_v_row(A, row, hh, t_begin);
         const size_t gs = (size_t)A.map.heads;
-        const int x = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens + t_begin;
         float carry = 1.f;  // product of the gates behind the chunk
         int bad = kNoBad;
         auto ask = [&](int i) {  // gates of the i-th chunk from the end
@@ -100,15 +117,6 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             const int at = (chunks - 1 - i) * C;
             const uint32_t st = (uint32_t)i % kLsStages;
             if (i >= kLsStages) wait(&bars->empty[st], (uint32_t)i / kLsStages - 1u);
-            if (lane == 0 && ok) {  // the loads first, the weights while they are under way
-                uint8_t *sp = smem + st * SH::STAGE;
-                mbar_expect_tx(&bars->full[st], SH::STAGE);
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    tma_load_2d(sp + kb * 8192, &mk, x + 64 * kb, y0 + at, &bars->full[st]);
-                    tma_load_2d(sp + SH::V + kb * 8192, &mv, xv + 64 * kb, y0 + at, &bars->full[st]);
-                }
-            }
             ask(i + kLsGates - 1);
             cp_async_wait<kLsGates - 1>();  // a lane reads what it asked for
             const float2 a = *reinterpret_cast<const float2 *>(smem + SH::G + (i % kLsGates) * 256 + 8 * lane);
