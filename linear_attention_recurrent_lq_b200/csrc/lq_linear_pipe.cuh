@@ -20,8 +20,8 @@
 //   0 .. 7   the state: scaled, and cut into the pieces of an A operand in
 //            tensor memory; read from and written to global memory
 //   8 .. 15  four for the outputs, from tensor memory to global memory, and
-//            four, with 20, 22 and 23, for K' = k / G, in three pieces to shared
-//            memory
+//            four, with 20, 22, 23 and 25 .. 27, for K' = k / G, in three pieces to
+//            shared memory
 //   16, 17, 21  the scores Q K^T, a block of 32 x 32 each: from tensor memory,
 //            times 1 / G, masked, in three pieces to shared memory
 //   18       one thread issues V^T K', S^T Q^T and V^T P^T
@@ -37,7 +37,7 @@
 
 namespace lq {
 
-constexpr int kLpThreads = 25 * 32;
+constexpr int kLpThreads = 28 * 32;
 constexpr int kLpRing = 4;     // chunk descriptions
 constexpr float kLpMinGate = 0x1p-64f;
 // tensor memory: Q K^T | O^T, two | S pieces | S
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         for (int i = 0; i < kLpRing; ++i) {
             ring[i].flags = kLpEnd;
             mbar_init(&bars->ring_full[i], 1);
-            mbar_init(&bars->ring_free[i], SH::SW + 14);  // output, key and score warps too
+            mbar_init(&bars->ring_free[i], SH::SW + 17);  // output, key and score warps too
         }
         mbar_init(&bars->qk_done, 1);
         mbar_init(&bars->qk_free, 3);
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         mbar_init(&bars->s_ready, SH::SW);
         mbar_init(&bars->y_done, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->k_ready[i], 7);
+            mbar_init(&bars->k_ready[i], 10);
             mbar_init(&bars->d_done[i], 1);
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->o_free[i], 4);
@@ -397,10 +397,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         }
         // every product has ended before tensor memory is given back
         if (warp == 18 && c > 0) mbar_wait_bounded(&bars->o_done[(c - 1u) & 1u], ((c - 1u) / 2u) & 1u);
-    } else if (warp == 20 || warp == 22 || warp == 23 || (warp >= 8 && warp < 16 && (D == 128 ? warp >= 12 : (warp & 3) >= 2))) {
+    } else if (warp == 20 || warp == 22 || warp == 23 || warp >= 25 || (warp >= 8 && warp < 16 && (D == 128 ? warp >= 12 : (warp & 3) >= 2))) {
         // ------------------------------------------------- k / G, in pieces
-        constexpr int NP = 8 * KB, NT = 7 * 32;
-        const int kw = warp == 20 ? 4 : warp >= 22 ? warp - 17 : D == 128 ? warp - 12 : (warp & 1) + (warp >= 12 ? 2 : 0);
+        constexpr int NP = 8 * KB, NT = 10 * 32;
+        const int kw = warp >= 25 ? warp - 18 : warp >= 22 ? warp - 17 : warp == 20 ? 4 : D == 128 ? warp - 12 : (warp & 1) + (warp >= 12 ? 2 : 0);
         const int kt = 32 * kw + lane;
         uint32_t c = 0;
 #pragma unroll 1

@@ -44,22 +44,24 @@ __device__ __forceinline__ void store_piece(void *p, const float (&x)[BF16 ? 8 :
     *reinterpret_cast<uint4 *>(p) = w;
 }
 
-// exp(-rate softplus(x)), softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|).
-// Small ones have to keep their digits, so log(1 + e) is not taken of a rounded
-// 1 + e but from its series 2 artanh(r), r = e / (2 + e) <= 1/3; the first
-// term left out is r^14 / 15 <= 1.4e-8 of the sum.  20 instructions; with
-// log1pf, expf and their branches the gates of a key-channel layer took as
-// long as its memory traffic twice.
-__device__ __forceinline__ float gate_decay(float x, float rate) {
-    const float e = __expf(-fabsf(x));
-    const float r = __fdividef(e, 2.f + e), r2 = r * r;
-    float p = fmaf(r2, 1.f / 13.f, 1.f / 11.f);
-    p = fmaf(r2, p, 1.f / 9.f);
-    p = fmaf(r2, p, 1.f / 7.f);
-    p = fmaf(r2, p, 1.f / 5.f);
-    p = fmaf(r2, p, 1.f / 3.f);
-    p = fmaf(r2, p, 1.f);
-    return __expf(-rate * (fmaxf(x, 0.f) + 2.f * r * p));
+// exp(-rate softplus(x)) of two, softplus(x) = max(x, 0) + log(1 + e), e =
+// exp(-|x|).  Small ones have to keep their digits, so log(1 + e) is not taken of
+// a rounded 1 + e but from its series 2 artanh(r), r = e / (2 + e) <= 1/3; the
+// first term left out is r^14 / 15 <= 1.4e-8 of the sum.  With log1pf and expf
+// the gates of a key-channel layer took as long as its memory traffic twice.
+__device__ __forceinline__ float2 gate_decay2(float2 x, float rate) {
+    const float2 e = make_float2(__expf(-fabsf(x.x)), __expf(-fabsf(x.y)));
+    const float2 r = make_float2(__fdividef(e.x, 2.f + e.x), __fdividef(e.y, 2.f + e.y)), r2 = __fmul2_rn(r, r);
+    auto both = [](float c) { return make_float2(c, c); };
+    float2 p = __ffma2_rn(r2, both(1.f / 13.f), both(1.f / 11.f));
+    p = __ffma2_rn(r2, p, both(1.f / 9.f));
+    p = __ffma2_rn(r2, p, both(1.f / 7.f));
+    p = __ffma2_rn(r2, p, both(1.f / 5.f));
+    p = __ffma2_rn(r2, p, both(1.f / 3.f));
+    p = __ffma2_rn(r2, p, both(1.f));
+    const float2 soft = __ffma2_rn(__fmul2_rn(both(2.f), r), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+    const float2 t = __fmul2_rn(both(-rate), soft);
+    return make_float2(__expf(t.x), __expf(t.y));
 }
 
 __device__ __forceinline__ float sigmoidf(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
@@ -130,6 +132,9 @@ __global__ void __launch_bounds__(256) qk_norm_kernel(QkNormArgs A) {
     }
     if (A.kda) {  // V channels of one head
         const unsigned r0 = gates * (G * kGateUnroll) + tid / LR;  // rows * H < 2^31
+        // heads of the rows u G apart: one division, then steps
+        unsigned h = r0 % (unsigned)A.H;
+        const unsigned step = G % (unsigned)A.H;
         uint4 w[kGateUnroll];
 #pragma unroll
         for (int u = 0; u < kGateUnroll; ++u) {
@@ -141,25 +146,27 @@ __global__ void __launch_bounds__(256) qk_norm_kernel(QkNormArgs A) {
         for (int u = 0; u < kGateUnroll; ++u) {
             const unsigned r = r0 + u * G;
             if (r >= A.heads_n) return;
-            const unsigned h = r % (unsigned)A.H;
             const float rate = __expf(A.a_log[h]);
             float x[V];
             unpack_piece<BF16>(w[u], x);
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
                 const float4 d = __ldg(reinterpret_cast<const float4 *>(A.dt_bias + (size_t)h * D + c + i));
-                const float4 g = make_float4(gate_decay(x[i] + d.x, rate), gate_decay(x[i + 1] + d.y, rate),
-                                             gate_decay(x[i + 2] + d.z, rate), gate_decay(x[i + 3] + d.w, rate));
-                *reinterpret_cast<float4 *>(A.decay + (size_t)r * D + c + i) = g;
+                const float2 g0 = gate_decay2(__fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(d.x, d.y)), rate);
+                const float2 g1 = gate_decay2(__fadd2_rn(make_float2(x[i + 2], x[i + 3]), make_float2(d.z, d.w)), rate);
+                *reinterpret_cast<float4 *>(A.decay + (size_t)r * D + c + i) = make_float4(g0.x, g0.y, g1.x, g1.y);
             }
             if (c == 0) A.beta[r] = sigmoidf(load_in(A.b, (size_t)r, BF16));
+            h += step;
+            if (h >= (unsigned)A.H) h -= (unsigned)A.H;
         }
         return;
     }
     const unsigned x = gates * 256u + tid;
     if (x >= A.heads_n) return;
     const unsigned h = x % (unsigned)A.H;
-    A.decay[x] = gate_decay(load_in(A.a, (size_t)x, BF16) + A.dt_bias[h], expf(A.a_log[h]));
+    const float z = load_in(A.a, (size_t)x, BF16) + A.dt_bias[h];
+    A.decay[x] = gate_decay2(make_float2(z, z), expf(A.a_log[h])).x;
     A.beta[x] = sigmoidf(load_in(A.b, (size_t)x, BF16));
 }
 

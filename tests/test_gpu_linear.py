@@ -482,3 +482,45 @@ def test_offsets_beyond_32_bits():
     near(out[:, -tail:], want, "last tokens")
     near(st.dequant(), S, "last state")
     assert st.check() == b.LQ_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("t", [3, 70, 150])
+def test_non_finite_rows_stay_in_their_head(t, d, dtype):
+    """Infinities and NaN in some heads' q, k or v leave every other head right,
+    also where one SM takes them one after the other."""
+    n, h = 170, 2
+    x = inputs(70, n, t, h, h, d, DT[dtype])
+    want, S = reference(x, x["S0"])
+    bad = torch.zeros(n, h, dtype=torch.bool, device="cuda")
+    for i, (row, head, name, value) in enumerate([(0, 0, "v", float("nan")), (3, 1, "k", float("inf")), (90, 0, "q", float("-inf")),
+                                                  (150, 1, "v", float("inf")), (169, 0, "k", float("nan"))]):
+        x[name][row, min(i, t - 1), head, 5] = value
+        bad[row, head] = True
+    st = state_of(n, h, d, DT[dtype])
+    for S0 in (x["S0"], None):
+        if S0 is None:
+            want, S = reference({k: v[~bad.any(1)] for k, v in x.items()}, None)
+            out = run_prefill(st, x)
+            near(out[~bad.any(1)], want)
+            near(st.dequant()[~bad.any(1)], S)
+        else:
+            out = run_prefill(st, x, S0=S0)
+            good = ~bad
+            near(out.transpose(1, 2)[good], want.transpose(1, 2)[good])
+            near(st.dequant()[good], S[good])
+    assert st.check() == 0
+
+
+def test_a_state_on_a_given_buffer():
+    b = B()
+    cfg = b.make_config(2, 3, 64, 64, bits=32)
+    buf = torch.zeros(2 * 3 * b.lq_state_bytes(cfg) + 256, dtype=torch.uint8, device="cuda")
+    st = b.LQState(cfg, buf=buf)
+    x = inputs(71, 2, 1, 3, 3, 64, torch.bfloat16)
+    st.init(x["S0"])
+    assert st.ptr == buf.data_ptr() and torch.equal(st.dequant(), x["S0"])
+    short = b.LQState(cfg, buf=buf[:1024])
+    with pytest.raises(ValueError, match="state"):
+        short.init(x["S0"])
