@@ -359,8 +359,8 @@ LQ_API lq_status lq_copy_slots(const lq_config *cfg, void *dst, int dst_num_slot
 LQ_API lq_status lq_linear_step(const lq_config *cfg, void *state, int qk_heads, const void *q, const void *k,
                                 const void *v, const float *decay, float *out, lq_stream_t stream);
 
-/* The same for the slots in `slots` (n_active rows in place of N; a row whose
- * slot is out of range gets zero outputs). */
+/* The same for the slots in `slots` (n_active rows in place of N, distinct
+ * entries; a row whose slot is out of range gets zero outputs). */
 LQ_API lq_status lq_linear_step_slots(const lq_config *cfg, void *state, const int32_t *slots, int n_active,
                                       int qk_heads, const void *q, const void *k, const void *v, const float *decay,
                                       float *out, lq_stream_t stream);
@@ -392,7 +392,8 @@ LQ_API lq_status lq_linear_prefill(const lq_config *cfg, void *state, int tokens
                                    const float *decay, float *out, uint32_t flags, void *workspace,
                                    size_t workspace_bytes, lq_stream_t stream);
 
-/* The same for the slots in `slots` (n_active rows in place of N). */
+/* The same for the slots in `slots` (n_active rows in place of N, distinct
+ * entries; a row whose slot is out of range gets zero outputs). */
 LQ_API lq_status lq_linear_prefill_slots(const lq_config *cfg, void *state, const int32_t *slots, int n_active,
                                          int tokens, const int32_t *lengths, const float *S0, int qk_heads,
                                          const void *q, const void *k, const void *v, const float *decay, float *out,

@@ -17,32 +17,53 @@ namespace {
 
 constexpr int kSms = 148;
 
-// Whether a bf16 prompt takes the chunkwise form on the tensor cores.  It costs
-// a chunk of 64 tokens whatever the prompt's length; token after token the time
-// grows with the tokens, but few heads spread over more SMs.  Measured, d = 128:
-// 12 heads, 48 tokens 15.2 us chunkwise and 13.2 us token after token, 64 tokens
-// 15.2 and 13.2; 48 heads, 64 tokens 12.3 and 18.4; 128 heads, 4 tokens 15.4 and
-// 19.4.  d = 64: 12 heads, 64 tokens
-// 11.2 and 12.3; 256 heads, 16 tokens 17.4 and 17.4; 2048 heads, 32 tokens 66.6
-// and 60.3, 48 tokens 66.6 and 76.8.
-bool chunked(const lq_config &c, int64_t work, int tokens) {
-    if (c.in_dtype != 1) return false;
-    if (work * (c.dk / 16) <= kSms) return tokens >= 65;  // a CTA of 16 columns for each SM
-    return tokens >= (c.dk == 128 && work >= kSms / 2 ? 4 : 33);
+// Token after token, a CTA takes 16, 64 or (d = 128) 128 columns of a head.
+// Of 16: the latency of a token is lowest, but a cluster of 4 or 8 CTAs reads
+// each q and k anew.  f32, 200 tokens, 16 and 64 columns: d = 128, 12 heads 25.1
+// and 43.8 us, 24 heads 39.4 and 43.9, 36 heads 67.9 and 44.2; d = 64, 24 heads
+// 17.3 and 24.5, 36 heads 24.9 and 24.6, 74 heads 39.6 and 24.6.
+bool narrow(const lq_config &c, int64_t work) { return work * (c.dk / 16) <= kSms * 4 / 3; }
+
+// Of 128 columns, eight per lane: shared memory is read half as often.  What
+// decides is how many CTAs an SM gets.  f32, 200 tokens, 64 and 128 columns: 74
+// heads 44.5 and 60.6 us, 100 heads 64.6 and 60.8, 140 heads 86.4 and 61.1, 200
+// heads 88.3 and 101.5, 296 heads 121 and 102, 600 heads 251 and 242.
+bool wide(const lq_config &c, int64_t work) {
+    return c.dv == 128 && work > kSms / 2 && (work <= kSms || work > 3 * kSms / 2);
 }
 
-// Token after token with d = 128: whether a CTA takes all 128 columns (eight per
-// lane, so that shared memory is read half as often) and not 64.  f32, 2048
-// heads of 256 tokens: 831 us and 962 us; 16 heads of 8192 tokens, cut along
-// time: 342 and 400; 3 heads of 300 tokens: 31 and 22.
-bool wide(const lq_config &c, int64_t work, int tokens) {
-    return c.dv == 128 && (work >= 2 * kSms || tokens >= 512);
+// Whether a bf16 prompt takes the chunkwise form on the tensor cores.  It costs
+// a chunk of 64 tokens whatever the prompt's length; token after token the time
+// grows with the tokens.  Chunkwise and token after token, d = 128: 12 heads, 64
+// tokens 11.0 and 7.8 us, 100 tokens 13.2 and 11.5, 128 tokens (nothing in L2)
+// 14.3 and 18.4; 24 heads, 64 tokens 11.1 and
+// 10.7, 100 tokens 13.3 and 16.4; 60 heads, 17 tokens 8.2 and 6.8, 32 tokens 8.3
+// and 8.6; 140 heads, 8 tokens 9.0 and 6.7, 17 tokens 9.1 and 10.4; 600 heads, 4
+// tokens 20.1 and 16.8, 8 tokens 19.8 and 20.8.  d = 64: 24 heads, 100 tokens 10.7
+// and 8.8, 200 tokens 16.3 and 15.0; 100 heads, 48 tokens 9.7 and 8.2, 64 tokens
+// 9.7 and 10.0; 2048 heads, 48 tokens 80 and 63, 64 tokens 78.7 and 80.3.
+bool chunked(const lq_config &c, int64_t work, int tokens) {
+    if (c.in_dtype != 1) return false;
+    // all clusters of 16-column CTAs at once, an SM each (a few SMs stay outside)
+    if (work * (c.dk / 16) <= 128) return tokens > (c.dk == 128 ? 96 : 128);
+    if (c.dk == 64) return tokens >= 64;
+    if (narrow(c, work)) return tokens > 64;
+    return tokens >= 32 || (tokens >= 8 && work * tokens >= 2000);
 }
 
 // Where the heads alone leave SMs idle, a prompt is cut along time into `nseg`
 // segments of `seg_len` tokens.  That costs a pass over k and v for what the
 // segments leave behind, and a scan over those states.
 constexpr int kMaxSegments = 64;
+
+// Token after token: segments of 32 tokens or more.
+int64_t most_segments(int tokens) { return tokens / 32 < kMaxSegments ? tokens / 32 : kMaxSegments; }
+
+// The CTAs of a prompt cut along time, token after token, d = 128: 128 columns
+// where there are enough for two per SM.  64 and 128 columns: 8 heads of 777
+// tokens 46 and 52 us, 24 heads of 400 tokens 49 and 55; 8 heads of 2000 tokens
+// 76 and 68, 36 heads 220 and 202.
+bool wide_cut(const lq_config &c, int64_t work, int tokens) { return c.dv == 128 && work * most_segments(tokens) > 300; }
 
 struct Cut {
     int seg_len, nseg;
@@ -72,13 +93,26 @@ Cut cut_of(const lq_config &c, int64_t work, int tokens) {
         }
         return best;
     }
-    // Token after token: six CTAs (of 64 columns) per SM, with d = 128 three, or
-    // two of 128 columns; segments of 32 tokens or more.  f32, d = 64, 36 heads
-    // of 777 tokens: 36 us so, 44 us with three per SM and 64 tokens
-    const int64_t per_sm = c.dv == 64 ? 6 : wide(c, work, tokens) ? 2 : 3, ctas = work * (per_sm == 3 ? 2 : 1);
-    int64_t n = per_sm * kSms / ctas;
-    if (n > tokens / 32) n = tokens / 32;
-    if (n > kMaxSegments) n = kMaxSegments;
+    // Token after token (f32).  Both passes together take about 0.85 ns (d = 128:
+    // 2.5 ns) per head and token and 15 us (22), the uncut prompt 113 ns (210) per
+    // token.  Cut and uncut, d = 64: 74 heads of 256 tokens 31 and 32 us, 100 heads
+    // 39 and 32, 100 heads of 2000 tokens 171 and 225, 148 heads 224 and 226;
+    // d = 128: 36 heads of 256 tokens 49 and 57 us, 50 heads of 777 tokens 124 and
+    // 164, 64 heads of 400 tokens 99 and 87, 74 heads of 2000 tokens 385 and 422,
+    // 148 heads 638 and 569.
+    const int64_t most = most_segments(tokens);
+    int64_t n;
+    if (c.dv == 64) {
+        if (work * tokens >= 133 * (int64_t)tokens - 14000) return best;
+        n = 6 * kSms / work;  // CTAs per SM: 36 heads of 777 tokens 36 us, with three 47 us
+    } else {
+        if (work * tokens >= 84 * (int64_t)tokens - 8800) return best;
+        // CTAs of 128 columns two per SM, or twice as many: 36 heads of 2000 tokens
+        // 202 us in 8 segments and 213 in 16, 64 heads 379 in 4 and 353 in 12
+        n = most;
+        if (wide_cut(c, work, tokens)) n = (2 * kSms / work >= 6 ? 2 : 4) * kSms / work;
+    }
+    if (n > most) n = most;
     if (n < 2) return best;
     best.seg_len = (int)align_up((uint32_t)((tokens + n - 1) / n), 16u);
     best.nseg = (tokens + best.seg_len - 1) / best.seg_len;
@@ -103,8 +137,12 @@ lq_status check_linear(const lq_config *cfg, int qk_heads) {
 
 template <int D, bool BF16>
 lq_status launch_step(const LinArgs &a, cudaStream_t s) {
-    // few heads: four CTAs per head, so that every SM has loads in flight
-    if (a.work < 2 * kSms) return launched(launch_pdl(lin_step_kernel<D, BF16, D / 4>, a.work * 4, 256, 0u, s, a));
+    // d = 128, few heads: four CTAs per head, so that every SM has loads in flight.
+    // Four and one: 12 heads 1.8 and 2.6 us, 148 heads 4.9 and 4.9, 280 heads 7.4
+    // and 8.1, 400 heads 9.8 and 10.0; d = 64, 32 heads 1.7 and 1.8, 200 heads 3.8
+    // and 3.0
+    if constexpr (D == 128)
+        if (a.work < 2 * kSms) return launched(launch_pdl(lin_step_kernel<D, BF16, D / 4>, a.work * 4, 256, 0u, s, a));
     return launched(launch_pdl(lin_step_kernel<D, BF16, D>, a.work, 256, 0u, s, a));
 }
 
@@ -133,7 +171,7 @@ lq_status step_rows(const lq_config &c, void *state, const int32_t *slots, int r
 template <int D, bool BF16, int C>
 lq_status launch_recurrent(const LinArgs &a, cudaStream_t s) {
     using SH = LinShape<D, BF16, C>;
-    if (a.nseg > 1) {
+    if constexpr (!BF16 && C > 1) if (a.nseg > 1) {  // others are not cut (cut_of)
         auto k = lin_recurrent_kernel<D, BF16, C, true>;
         if (allow_smem(k, SH::SMEM) != cudaSuccess) return LQ_ERR_CUDA;
         if (launch_pdl(k, dim3((unsigned)(a.work * SH::NB), (unsigned)(a.nseg - 1)), kLinThreads, 1, SH::SMEM, s,
@@ -193,10 +231,9 @@ template <int D, bool BF16>
 lq_status launch_prefill(const lq_config &c, const LinArgs &a, cudaStream_t s) {
     if constexpr (BF16)
         if (chunked(c, a.work, a.tokens)) return launch_chunked<D>(a, s);
-    // a short prompt of few heads: 16 columns per CTA
-    if (a.nseg == 1 && (int64_t)a.work * (D / 64) < 2 * kSms) return launch_recurrent<D, BF16, 1>(a, s);
+    if (a.nseg == 1 && narrow(c, a.work)) return launch_recurrent<D, BF16, 1>(a, s);
     if constexpr (D == 128)
-        if (wide(c, a.work, a.tokens)) return launch_recurrent<D, BF16, 8>(a, s);
+        if (a.nseg == 1 ? wide(c, a.work) : wide_cut(c, a.work, a.tokens)) return launch_recurrent<D, BF16, 8>(a, s);
     return launch_recurrent<D, BF16, 4>(a, s);
 }
 

@@ -319,6 +319,37 @@ def test_prefill_cut_along_time(n, h, d, t, dtype):
     near(o, want, "own workspace")
 
 
+@pytest.mark.parametrize("n,h,hk,d,t,dtype", [
+    (10, 10, 5, 128, 19, "f32"), (23, 10, 10, 128, 5, "f32"), (15, 10, 2, 128, 37, "f32"), (4, 10, 10, 128, 40, "f32"),
+    (2, 12, 12, 128, 70, "f32"), (7, 11, 11, 64, 33, "f32"), (8, 2, 1, 128, 700, "f32"), (5, 8, 8, 128, 515, "f32"),
+    (6, 10, 10, 64, 300, "f32"), (1, 8, 8, 128, 777, "f32"), (10, 14, 7, 64, 256, "f32"), (1, 25, 25, 128, 31, "bf16"),
+    (1, 25, 25, 128, 32, "bf16"), (10, 10, 10, 128, 19, "bf16"), (10, 10, 10, 128, 20, "bf16"), (30, 10, 10, 128, 7, "bf16"),
+    (30, 10, 10, 128, 8, "bf16"), (1, 12, 12, 128, 96, "bf16"), (1, 12, 12, 128, 97, "bf16"),
+    (2, 16, 8, 64, 128, "bf16"), (2, 16, 8, 64, 129, "bf16"), (20, 10, 10, 64, 63, "bf16")])
+def test_prefill_on_both_sides_of_each_choice(n, h, hk, d, t, dtype):
+    """Head counts and lengths around those that change a prompt's kernel or its
+    cut: given, continued and with a bad gate in two heads."""
+    x = inputs(11, n, t, h, hk, d, DT[dtype])
+    x["decay"][:, t // 3, ::3] = 0
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, DT[dtype])
+    near(run_prefill(st, x, S0=x["S0"]), want, "given")
+    near(st.dequant(), S, "state")
+    st.init(x["S0"])
+    near(run_prefill(st, x, cont=True), want, "continued")
+    near(st.dequant(), S, "continued state")
+    assert st.check() == 0
+    for row, head, at in ((0, 0, t - 1), (n - 1, h - 1, t // 2)):
+        x["decay"][row, at, head] = -1.0
+        early, Se = reference({k: v[row:row + 1, :at] if k != "S0" else v for k, v in x.items()}, x["S0"][row:row + 1])
+        want[row, :, head] = 0
+        want[row, :at, head] = early[0, :, head]
+        S[row, head] = Se[0, head]
+    near(run_prefill(st, x, S0=x["S0"]), want, "bad gates")
+    near(st.dequant(), S, "state before the bad gates")
+    assert st.check() == B().LQ_ERR_RANGE
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("t", [40, 1200])
 def test_prefill_slots(t, dtype):
