@@ -36,12 +36,12 @@ bool wide(const lq_config &c, int64_t work) {
 // a chunk of 64 tokens whatever the prompt's length; token after token the time
 // grows with the tokens.  Chunkwise and token after token, d = 128: 12 heads, 64
 // tokens 11.0 and 7.8 us, 100 tokens 13.2 and 11.5, 128 tokens (nothing in L2)
-// 14.3 and 18.4; 24 heads, 64 tokens 11.1 and
-// 10.7, 100 tokens 13.3 and 16.4; 60 heads, 17 tokens 8.2 and 6.8, 32 tokens 8.3
-// and 8.6; 140 heads, 8 tokens 9.0 and 6.7, 17 tokens 9.1 and 10.4; 600 heads, 4
-// tokens 20.1 and 16.8, 8 tokens 19.8 and 20.8.  d = 64: 24 heads, 100 tokens 10.7
-// and 8.8, 200 tokens 16.3 and 15.0; 100 heads, 48 tokens 9.7 and 8.2, 64 tokens
-// 9.7 and 10.0; 2048 heads, 48 tokens 80 and 63, 64 tokens 78.7 and 80.3.
+// 14.3 and 18.4; 24 heads, 64 tokens 11.1 and 10.7, 100 tokens 13.3 and 16.4; 60
+// heads, 17 tokens 8.2 and 6.8, 32 tokens 8.3 and 8.6; 140 heads, 8 tokens 9.0
+// and 6.7, 17 tokens 9.1 and 10.4; 600 heads, 4 tokens 20.1 and 16.8, 8 tokens
+// 19.8 and 20.8.  d = 64: 24 heads, 100 tokens 10.7 and 8.8, 200 tokens 16.3 and
+// 15.0; 100 heads, 48 tokens 9.7 and 8.2, 64 tokens 9.7 and 10.0; 2048 heads, 48
+// tokens 80 and 63, 64 tokens 78.7 and 80.3.
 bool chunked(const lq_config &c, int64_t work, int tokens) {
     if (c.in_dtype != 1) return false;
     // all clusters of 16-column CTAs at once, an SM each (a few SMs stay outside)

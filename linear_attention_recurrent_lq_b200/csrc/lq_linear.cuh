@@ -119,7 +119,8 @@ __device__ __forceinline__ float4 lin_load4(const uint8_t *p) {
 // ------------------------------------------------------------- one token
 // Bound by HBM: the state is read and written once.  A CTA takes CB columns
 // of one head, all its loads in flight before the first use, a thread four
-// columns of R rows.
+// columns of R rows.  d = 128: 64 x 32 heads 43.1 us, 6290 GB/s (41.4 us at the
+// copy's rate), 512 x 36 heads through a slot list 290.6 us (279.4).
 template <int D, bool BF16, int CB>
 __global__ void __launch_bounds__(256, 3) lin_step_kernel(LinArgs A) {
     constexpr int E = BF16 ? 2 : 4, NB = D / CB, CQ = CB / 4, RG = 256 / CQ, R = D / RG;
@@ -193,7 +194,9 @@ __global__ void __launch_bounds__(256, 3) lin_step_kernel(LinArgs A) {
 //     S / G_t += k_t (v_t / G_t),   o_t = G_t (S / G_t)^T q_t,
 // and S is brought back to G = 1 before 16 tokens that start from G < 2^-32.
 // 16 tokens whose gates multiply to less than 2^-60 (gates of 0 among them)
-// are taken one by one from G = 1: S = a_t S + k_t v_t^T.
+// are taken one by one from G = 1: S = a_t S + k_t v_t^T.  f32, 2048 heads of 256
+// tokens: d = 128 833 us, 462 of them multiply-adds at their peak rate; d = 64
+// 266 us (115); the rest are reads of q, k and v from shared memory.
 constexpr int kLinTokens = 16;  // tokens per stage
 constexpr int kLinStages = 3;
 constexpr int kLinThreads = 128;
