@@ -350,7 +350,8 @@ LQ_API lq_status lq_copy_slots(const lq_config *cfg, void *dst, int dst_num_slot
  * Alignment: q, k, v, S0, out and workspace 16 bytes, decay, slots and
  * lengths 4.  A non-finite q, k or v makes its head's state non-finite, as
  * the formula has it; in a prompt it may also reach outputs of the same head
- * up to 63 tokens before it. */
+ * up to 63 tokens before it.  Prompts hold the state over a product of gates of
+ * 2^-64 or more, so a state or k v^T beyond 2^63 may overflow there. */
 
 /* One token for every (slot, head).
  *   q, k [N, Hk, dk]  v [N, H, dv] in_dtype   decay [N, H]   out [N, H, dv] f32

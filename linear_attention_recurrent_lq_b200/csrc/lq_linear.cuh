@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(256, 3) lin_step_kernel(LinArgs A) {
 // Bound by FP32 multiply-adds.  The registers hold S / G with G the product of
 // the gates so far, so a token costs two per entry instead of three,
 //     S / G_t += k_t (v_t / G_t),   o_t = G_t (S / G_t)^T q_t,
-// and S is brought back to G = 1 before 16 tokens that start from G < 2^-32.
-// 16 tokens whose gates multiply to less than 2^-60 (gates of 0 among them)
+// and S is brought back to G = 1 before 16 tokens that start from G < 2^-16.
+// 16 tokens whose gates multiply to less than 2^-48 (gates of 0 among them)
 // are taken one by one from G = 1: S = a_t S + k_t v_t^T.  f32, 2048 heads of 256
 // tokens: d = 128 833 us, 462 of them multiply-adds at their peak rate; d = 64
 // 266 us (115); the rest are reads of q, k and v from shared memory.
@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kLinThreads, C == 8 ? 2 : 4) lin_recurrent_ker
             if ((lane & (TB - 1)) >= d) pre *= x;
         }
         const float total = __shfl_sync(0xFFFFFFFFu, pre, TB - 1);
-        const bool apart = !(total >= 0x1p-60f);
-        if (apart || G < 0x1p-32f) {
+        const bool apart = !(total >= 0x1p-48f);
+        if (apart || G < 0x1p-16f) {
             const float2 g2 = make_float2(G, G);
 #pragma unroll
             for (int p = 0; p < 2 * M; ++p)

@@ -516,6 +516,23 @@ def test_offsets_beyond_32_bits():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,d,t", [(1, 64, 40), (2, 128, 150), (60, 128, 70), (130, 128, 33), (1, 128, 700), (1, 64, 700)])
+@pytest.mark.parametrize("gate", [0.06, 0.3, 0.9])
+def test_large_values_under_strong_gates(n, d, t, gate, dtype):
+    """Values of 2^55 stay finite whatever the gates: the state is held over a
+    product of gates of 2^-64 or more."""
+    x = inputs(72, n, t, 2, 2, d, DT[dtype])
+    x["v"] = x["v"] * 2.0 ** 55
+    x["S0"] = x["S0"] * 2.0 ** 55
+    x["decay"] = gate * x["decay"]
+    want, S = reference(x, x["S0"])
+    st = state_of(n, 2, d, DT[dtype])
+    near(run_prefill(st, x, S0=x["S0"]), want)
+    near(st.dequant(), S)
+    assert st.check() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("t", [3, 70, 150])
 def test_non_finite_rows_stay_in_their_head(t, d, dtype):
