@@ -94,11 +94,11 @@ Cut cut_of(const lq_config &c, int64_t work, int tokens) {
         return best;
     }
     // Token after token (f32).  Both passes together take about 0.85 ns (d = 128:
-    // 2.5 ns) per head and token and 15 us (22), the uncut prompt 113 ns (210) per
+    // 2.5 ns) per head and token and 15 us (28), the uncut prompt 113 ns (210) per
     // token.  Cut and uncut, d = 64: 74 heads of 256 tokens 31 and 32 us, 100 heads
     // 39 and 32, 100 heads of 2000 tokens 171 and 225, 148 heads 224 and 226;
-    // d = 128: 36 heads of 256 tokens 49 and 57 us, 50 heads of 777 tokens 124 and
-    // 164, 64 heads of 400 tokens 99 and 87, 74 heads of 2000 tokens 385 and 422,
+    // d = 128: 36 heads of 256 tokens 53 and 57 us, 50 heads of 777 tokens 124 and
+    // 164, 60 heads of 400 tokens 103 and 87, 74 heads of 2000 tokens 385 and 422,
     // 148 heads 638 and 569.
     const int64_t most = most_segments(tokens);
     int64_t n;
@@ -106,7 +106,7 @@ Cut cut_of(const lq_config &c, int64_t work, int tokens) {
         if (work * tokens >= 133 * (int64_t)tokens - 14000) return best;
         n = 6 * kSms / work;  // CTAs per SM: 36 heads of 777 tokens 36 us, with three 47 us
     } else {
-        if (work * tokens >= 84 * (int64_t)tokens - 8800) return best;
+        if (work * tokens >= 84 * (int64_t)tokens - 11500) return best;
         // CTAs of 128 columns two per SM, or twice as many: 36 heads of 2000 tokens
         // 202 us in 8 segments and 213 in 16, 64 heads 379 in 4 and 353 in 12
         n = most;
