@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 
                 const uint32_t st = c % ST;
                 if (c >= ST) wait(&bars->empty[st], c / ST - 1u);
-                if (ok && lc_elect()) {
+                if (!ok) break;  // c counts what has been asked for
+                if (lc_elect()) {
                     uint8_t *sp = smem + st * SH::STAGE;
                     bars->from_zero[st] = from_zero && t0 == t_begin;
                     mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         }
         arrive(&bars->ring_full[r % kLpRing]);
         // what has been asked for lands before the CTA leaves
-        for (uint32_t i = c >= ST ? c - ST + 1u : 0u; i < c; ++i) wait(&bars->full[i % ST], i / ST);
+        for (uint32_t i = c >= ST ? c - ST : 0u; i < c; ++i) wait(&bars->full[i % ST], i / ST);
         if (c >= ST) wait(&bars->empty[c % ST], c / ST - 1u);
         arrive(&bars->full[c % ST]);  // warp 24 learns the end here
     } else if (warp == 18 || warp == 24) {
@@ -330,6 +331,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const uint32_t td = uni(tmem), q0 = uni(lc_desc(base, 16u));
         const volatile uint32_t *chunks = &bars->chunks;
         uint32_t c = 0, st = 0, full_ph = 0;
+        // Whatever a commit arrives on has to be waited for before the CTA gives its
+        // shared memory and tensor memory back, by the warp that made the commit: the
+        // last ones have no other waiter, and after a wait that gave up none may have.
+        auto landed = [](uint64_t *b, uint32_t phase) { mbar_wait_bounded(b, phase & 1u); };
         if (warp == 24) {
 #pragma unroll 1
             for (; ok; ++c) {
@@ -352,9 +357,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     full_ph ^= 1u;
                 }
             }
+            if (c > 0) landed(&bars->qk_done, c - 1u);
         } else {
             const uint32_t pd = uni(lc_desc(base + SH::P, 16u)), v0 = uni(lc_desc(base + SH::V, vlbo)),
                            k0 = uni(lc_desc(base + SH::K, 8192u));
+            uint32_t begun = 0;  // chunks whose first products were issued; c: whose last were
 #pragma unroll 1
             for (; ok; ++c) {
                 const uint32_t at = uni(st * (SH::STAGE / 16u)), o = uni(td + kLpO + 64u * (c & 1u));
@@ -384,6 +391,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     }
                     umma_commit(&bars->y_done);
                 }
+                begun = c + 1u;
                 __syncwarp();
                 wait(&bars->p_ready, c);
                 if (!ok) break;
@@ -401,9 +409,13 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 __syncwarp();
                 if (++st == (uint32_t)ST) st = 0;
             }
+            // a barrier's earlier phase had ended when its last commit was made (the
+            // operands of that chunk waited for it), so the parity is not ambiguous
+            for (uint32_t i = begun > NK ? begun - NK : 0u; i < begun; ++i) landed(&bars->d_done[i % NK], i / NK);
+            if (begun > 0) landed(&bars->y_done, begun - 1u);
+            for (uint32_t i = c > 2u ? c - 2u : 0u; i < c; ++i) landed(&bars->o_done[i & 1u], i / 2u);
+            for (uint32_t i = c > ST ? c - ST : 0u; i < c; ++i) landed(&bars->empty[i % ST], i / ST);
         }
-        // every product has ended before tensor memory is given back
-        if (warp == 18 && c > 0) mbar_wait_bounded(&bars->o_done[(c - 1u) & 1u], ((c - 1u) / 2u) & 1u);
     } else if (warp == 20 || warp == 22 || warp == 23 || warp >= 25 || (warp >= 8 && warp < 16 && (D == 128 ? warp >= 12 : (warp & 3) >= 2))) {
         // ------------------------------------------------- k / G, in pieces
         constexpr int NP = 8 * KB, NT = 10 * 32;

@@ -85,11 +85,13 @@ __global__ void __launch_bounds__(kLsThreads, 1)
 
     if (warp == kLsKeys + 2) {  // the loads
         const int x = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens + t_begin;
+        int i = 0;  // loads asked for
 #pragma unroll 1
-        for (int i = 0; i < chunks && ok; ++i) {
+        for (; i < chunks; ++i) {
             const uint32_t st = (uint32_t)i % kLsStages;
             if (i >= kLsStages) wait(&bars->empty[st], (uint32_t)i / kLsStages - 1u);
-            if (ok && lc_elect()) {
+            if (!ok) break;
+            if (lc_elect()) {
                 uint8_t *sp = smem + st * SH::STAGE;
                 const int y = y0 + (chunks - 1 - i) * C;
                 mbar_arrive_expect_tx(&bars->full[st], SH::STAGE);
@@ -101,6 +103,8 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             }
             __syncwarp();
         }
+        // they land before the CTA leaves, also where nobody waits for them any more
+        for (int j = i > kLsStages ? i - kLsStages : 0; j < i; ++j) wait(&bars->full[j % kLsStages], (uint32_t)(j / kLsStages));
     } else if (warp == kLsKeys + 1) {  // the weights
         const float *gates = A.decay + lin_v_row(A, row, hh, t_begin);
         const size_t gs = (size_t)A.map.heads;
@@ -141,6 +145,7 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->full[st]);
         }
+        cp_async_wait<0>();
         if (lane == 0) {
             A.ws_g[(size_t)w * A.nseg + seg] = carry;
             A.ws_bad[(size_t)w * A.nseg + seg] = bad;
@@ -149,12 +154,14 @@ __global__ void __launch_bounds__(kLsThreads, 1)
         auto uni = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
         constexpr uint32_t id = lc_idesc(128, D, 1, 1), vlbo = KB > 1 ? 8192u : 0u;
         const uint32_t v0 = uni(lc_desc(base + SH::V, vlbo)), k0 = uni(lc_desc(base + SH::K, 8192u)), td = uni(tmem);
+        int i = 0;  // chunks whose products were issued
 #pragma unroll 1
-        for (int i = 0; i < chunks && ok; ++i) {
+        for (; i < chunks; ++i) {
             wait(&bars->k_ready[i & 1], (uint32_t)i / 2u);  // the chunk's loads have landed, too
+            if (!ok) break;
             const uint32_t vd = uni(v0 + (uint32_t)(i % kLsStages) * (SH::STAGE / 16u)), kd = uni(k0 + (uint32_t)(i & 1) * (SH::KBUF / 16u));
             const uint32_t acc = uni(i > 0 ? 1u : 0u);
-            if (ok && lc_elect()) {
+            if (lc_elect()) {
                 tc_fence_after();
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
@@ -168,6 +175,10 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             }
             __syncwarp();
         }
+        // every commit has arrived before shared memory and tensor memory are given back
+        for (int j = i > 2 ? i - 2 : 0; j < i; ++j) wait(&bars->d_done[j & 1], (uint32_t)j / 2u);
+        for (int j = i > kLsStages ? i - kLsStages : 0; j < i; ++j) wait(&bars->empty[j % kLsStages], (uint32_t)(j / kLsStages));
+        if (i == chunks) wait(&bars->all_done, 0u);
     } else {  // the keys, then the state to the workspace
         constexpr int NP = 8 * KB;
 #pragma unroll 1
