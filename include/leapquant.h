@@ -386,7 +386,8 @@ LQ_API size_t lq_linear_prefill_workspace(const lq_config *cfg, int rows, int to
  *            prompt is not cut).  Its content is not kept; calls that may run
  *            at the same time, graph replays too, need one each.
  * A prompt ends before its first bad gate (LQ_DEV_RANGE; zero outputs from
- * there on, the state holds the tokens before it). */
+ * there on, the state holds the tokens before it).  A (slot, head) whose
+ * status is LQ_DEV_TIMEOUT has neither outputs nor a state to use. */
 #define LQ_PREFILL_CONTINUE 0x1u
 LQ_API lq_status lq_linear_prefill(const lq_config *cfg, void *state, int tokens, const int32_t *lengths,
                                    const float *S0, int qk_heads, const void *q, const void *k, const void *v,

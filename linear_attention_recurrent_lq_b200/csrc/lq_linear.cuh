@@ -39,11 +39,12 @@ struct LinArgs {
     int seg_len, nseg;
     float *ws_S;   // [work, nseg, dk, dv]: a segment's own state, then the state before it
     float *ws_g;   // [work, nseg]: product of a segment's gates
-    int *ws_bad;   // [work, nseg]: its first token with a bad gate, INT_MAX if none
-    int *ws_run;   // [work]: 0 if the blob's header refuses the call
+    int *ws_bad;   // [work, nseg]: its first token with a bad gate, or kNoBad or kLost
+    int *ws_run;   // [work]: 0 if the blob's header refuses the call or a segment was lost
 };
 
-constexpr int kNoBad = 0x7FFFFFFF;
+constexpr int kNoBad = 0x7FFFFFFF;  // no gate is bad
+constexpr int kLost = -1;           // a wait of the first pass gave up: the segment's state is not there
 
 __device__ __forceinline__ bool lin_gate_ok(float a) { return a >= 0.f && a <= FLT_MAX; }
 
@@ -72,14 +73,21 @@ __device__ __forceinline__ const float *lin_state_source(const LinArgs &A, int w
     return A.S0 ? A.S0 + (size_t)w * (n / 4) : nullptr;
 }
 
-// Header of a blob whose prompt has been taken in.
-__device__ __forceinline__ void lin_write_header(uint8_t *blob, int cont, bool bad) {
-    if (cont) {
-        if (bad) set_status(blob, LQ_DEV_RANGE);
-        return;
-    }
-    *reinterpret_cast<uint4 *>(blob) = make_uint4(0u, bad ? LQ_DEV_RANGE : 0u, 0u, kMagic);
+// A new header with the given status.
+__device__ __forceinline__ void lin_new_header(uint8_t *blob, uint32_t status) {
+    *reinterpret_cast<uint4 *>(blob) = make_uint4(0u, status, 0u, kMagic);
     *reinterpret_cast<float *>(blob + kHdrG) = 1.f;
+}
+
+// Header of a blob whose prompt has been taken in.  That of a prompt cut along
+// time was written by the pass that joins the cuts: several CTAs add to its
+// status, so none of them may store it.
+__device__ __forceinline__ void lin_write_header(const LinArgs &A, uint8_t *blob, bool bad) {
+    if (A.cont || A.nseg > 1) {
+        if (bad) set_status(blob, LQ_DEV_RANGE);
+    } else {
+        lin_new_header(blob, bad ? LQ_DEV_RANGE : 0u);
+    }
 }
 
 // Whether a call that goes on from the blob may run; sets LQ_DEV_CORRUPT in a
@@ -257,20 +265,19 @@ __global__ void __launch_bounds__(kLinThreads, C == 8 ? 2 : 4) lin_recurrent_ker
     if (PARTIAL && bi < 0) return;
     uint8_t *blob = A.state + (size_t)(bi < 0 ? 0 : bi) * A.L.blob;
     bool run = bi >= 0;
-    if (!PARTIAL && A.cont) {
-        if (A.nseg > 1) {
-            run = run && A.ws_run[w] != 0;
-        } else {
-            if (run) run = lin_may_run(blob, tid == 0 && jc == 0);
-            // every CTA of the head reads the status before one may change it
-            if constexpr (SH::NB > 1)
-                asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (!PARTIAL && A.nseg > 1) {
+        if (run && seg <= last) {
+            run = A.ws_run[w] != 0;
+            for (int s = 0; s < seg; ++s)
+                if (A.ws_bad[(size_t)w * A.nseg + s] != kNoBad) run = false;
         }
+    } else if (!PARTIAL && A.cont) {
+        if (run) run = lin_may_run(blob, tid == 0 && jc == 0);
+        // every CTA of the head reads the status before one may change it
+        if constexpr (SH::NB > 1)
+            asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     }
     const int t_begin = seg * A.seg_len, t_end = min(A.tokens, t_begin + A.seg_len);
-    if (!PARTIAL && run && seg <= last)
-        for (int s = 0; s < seg; ++s)
-            if (A.ws_bad[(size_t)w * A.nseg + s] != kNoBad) run = false;
     const int t_stop = run ? min(len, t_end) : t_begin;
 
     // ---- the state this segment starts from
@@ -483,13 +490,16 @@ __global__ void __launch_bounds__(kLinThreads, C == 8 ? 2 : 4) lin_recurrent_ker
             lin_put_row<C>(dst + (size_t)i * D, a);
             lin_put_row<C>(dst + (size_t)(i + 1) * D, b);
         }
-        if (tid == 0 && jc == 0) lin_write_header(blob, A.cont, bad != kNoBad);
+        if (tid == 0 && jc == 0) lin_write_header(A, blob, bad != kNoBad);
     }
 }
 
 // ------------------------------------- joining a prompt cut along time
 // In place: each segment's own state becomes the state before that segment.
-// One thread takes four entries of one head through all segments.
+// One thread takes four entries of one head through all segments.  The first
+// CTA of a head also writes its header, before the main pass, whose CTAs only
+// add to the status; a head with a lost segment gets LQ_DEV_TIMEOUT and does
+// not run, so its outputs are zeros and its state stays as it was.
 template <int D>
 __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs A) {
     constexpr int NB = D * D / 1024;
@@ -501,16 +511,24 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs A) {
     if (bi < 0) return;
     uint8_t *blob = A.state + (size_t)bi * A.L.blob;
     float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int last = lin_last_segment(A, lin_length(A, row));
+    const bool run = !A.cont || lin_may_run(blob, e == 0);
+    if (blockIdx.x % NB == 0 && threadIdx.x < 32) {
+        bool lost = false;
+        for (int s = threadIdx.x; s < last; s += 32) lost |= A.ws_bad[(size_t)w * A.nseg + s] == kLost;
+        lost = __any_sync(0xFFFFFFFFu, lost);
+        if (threadIdx.x == 0) {
+            A.ws_run[w] = run && !lost;
+            if (!A.cont) lin_new_header(blob, lost ? LQ_DEV_TIMEOUT : 0u);
+            else if (run && lost) set_status(blob, LQ_DEV_TIMEOUT);
+        }
+    }
     if (A.cont) {
-        const bool one = e == 0;
-        const bool run = lin_may_run(blob, one);
-        if (one) A.ws_run[w] = run;
         if (!run) return;
         carry = *reinterpret_cast<const float4 *>(blob + kHdrBytes + 4 * (size_t)e);
     } else if (A.S0) {
         carry = *reinterpret_cast<const float4 *>(A.S0 + (size_t)w * (D * D) + e);
     }
-    const int last = lin_last_segment(A, lin_length(A, row));
     float *S = A.ws_S + (size_t)w * A.nseg * (D * D) + e;
     const float *g = A.ws_g + (size_t)w * A.nseg;
     // sixteen segments' loads in flight (one at a time: 30 us for 32 heads of 9

@@ -203,11 +203,12 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             const int bi = A.map.blob(w);
             uint8_t *blob = A.state + (size_t)(bi < 0 ? 0 : bi) * A.L.blob;
             bool run = bi >= 0;
-            if (A.cont && run) run = A.nseg > 1 ? A.ws_run[w] != 0 : lin_may_run(blob, lane == 0);
-            if (run && seg <= last) {
-                bool before = false;
-                for (int s = lane; s < seg; s += 32) before |= A.ws_bad[(size_t)w * A.nseg + s] != kNoBad;
-                if (__any_sync(0xFFFFFFFFu, before)) run = false;
+            if (A.nseg == 1) {
+                if (A.cont && run) run = lin_may_run(blob, lane == 0);
+            } else if (run && seg <= last) {
+                bool stop = A.ws_run[w] == 0;
+                for (int s = lane; s < seg; s += 32) stop |= A.ws_bad[(size_t)w * A.nseg + s] != kNoBad;
+                run = !__any_sync(0xFFFFFFFFu, stop);
             }
             const int t_begin = seg * A.seg_len, t_end = min(A.tokens, t_begin + A.seg_len);
             const int t_stop = run ? min(len, t_end) : t_begin;
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                     for (int y = 0; y < 16; ++y) dst[(size_t)(x + y) * D] = g * __uint_as_float(v[y]);
                 }
                 tc_fence_before();
-                if (tid == 0) lin_write_header(blob, A.cont, (flags & kLpBad) != 0);
+                if (tid == 0) lin_write_header(A, blob, (flags & kLpBad) != 0);
             }
             arrive(&bars->ring_free[r % kLpRing]);
         }

@@ -18,6 +18,9 @@
 // traffic; their 256 CTAs of 29 chunks are two rounds on 148 SMs, of 2100 clocks
 // a chunk (the keys' weights: 16 warps, the latency of a shared-memory round
 // trip and a split per chunk).
+//
+// A wait that gives up marks the segment as lost in the workspace: the blob's
+// header is written later, by the pass that joins the segments.
 #pragma once
 
 #include "lq_linear_mma.cuh"
@@ -121,10 +124,11 @@ __global__ void __launch_bounds__(kLsThreads, 1)
         };
         for (int i = 0; i < kLsGates - 1; ++i) ask(i);
 #pragma unroll 1
-        for (int i = 0; i < chunks && ok; ++i) {
+        for (int i = 0; i < chunks; ++i) {
             const int at = (chunks - 1 - i) * C;
             const uint32_t st = (uint32_t)i % kLsStages;
             if (i >= kLsStages) wait(&bars->empty[st], (uint32_t)i / kLsStages - 1u);
+            if (!ok) break;
             ask(i + kLsGates - 1);
             cp_async_wait<kLsGates - 1>();  // a lane reads what it asked for
             const float2 a = *reinterpret_cast<const float2 *>(smem + SH::G + (i % kLsGates) * 256 + 8 * lane);
@@ -182,13 +186,14 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     } else {  // the keys, then the state to the workspace
         constexpr int NP = 8 * KB;
 #pragma unroll 1
-        for (int i = warp / (kLsKeys / 2); i < chunks && ok; i += 2) {
+        for (int i = warp / (kLsKeys / 2); i < chunks; i += 2) {
             const uint32_t st = (uint32_t)i % kLsStages;
             // in this order: the products of chunk i - 2 stand behind those of
             // chunk i - 3, so the stage's phase before this one has ended for the
             // group that did not wait for it, too
             if (i >= 2) wait(&bars->d_done[i & 1], (uint32_t)i / 2u - 1u);
             wait(&bars->full[st], (uint32_t)i / kLsStages);
+            if (!ok) break;
             const float *W = reinterpret_cast<const float *>(smem + SH::W + st * 256u);
 #pragma unroll 2
             for (int x = tid % (kLsKeys * 16); x < C * NP; x += kLsKeys * 16) {
@@ -201,11 +206,11 @@ __global__ void __launch_bounds__(kLsThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->k_ready[i & 1]);
         }
-        wait(&bars->all_done, 0u);
+        if (ok) wait(&bars->all_done, 0u);
         tc_fence_after();
         constexpr int Q = D / (kLsKeys / 4);  // key channels of a warp
         const int j = 32 * (warp & 3) + lane, i0 = Q * (warp >> 2);
-        if ((warp & 3) < D / 32) {
+        if (ok && (warp & 3) < D / 32) {
             float *dst = A.ws_S + ((size_t)w * A.nseg + seg) * (D * D) + (size_t)i0 * D + j;
 #pragma unroll
             for (int x = 0; x < Q; x += 16) {
@@ -216,10 +221,9 @@ __global__ void __launch_bounds__(kLsThreads, 1)
                 for (int y = 0; y < 16; ++y) dst[(size_t)(x + y) * D] = __uint_as_float(v[y]);
             }
         }
-        if (!ok && lane == 0) set_status(A.state + (size_t)A.map.blob(w) * A.L.blob, LQ_DEV_TIMEOUT);
     }
     tc_fence_before();
-    __syncthreads();
+    if (__syncthreads_or(!ok) && tid == 0) A.ws_bad[(size_t)w * A.nseg + seg] = kLost;
     if (warp == kLsKeys) tmem_dealloc(tmem, 128u);
 }
 
