@@ -38,6 +38,11 @@
 // They meet in mbarriers only.  A barrier's waiters look at the parity of a
 // phase, so none may end twice before all have seen it once: where one side can
 // be a chunk ahead, there is a barrier for even and one for odd chunks.
+//
+// A role whose wait gives up leaves without an arrival, so its chunk's
+// description stays in the ring and the roles behind it give up, too.  What the
+// ring and the feeder then hold is what may be unfinished; those blobs get
+// LQ_DEV_TIMEOUT after the last role has left, when no header store can follow.
 #pragma once
 
 #include "lq_linear_mma.cuh"
@@ -79,6 +84,7 @@ struct LpBars {
     uint32_t tmem, chunks;  // chunks: how many there are, once the feeder knows
     uint64_t claim_done;
     uint32_t from_zero[4];  // per stage: the chunk starts from a zero state
+    int left[2];  // a feeder that gave up: the item it was at, and the one it had claimed
 };
 static_assert(sizeof(LpBars) <= 320, "barrier space");
 
@@ -99,9 +105,13 @@ __device__ __forceinline__ int claimed_cta(uint32_t answer) {  // -1: none is le
     return got ? (int)x : -1;
 }
 
+// Work item w may be unfinished; its header may not have been written yet.
 __device__ __forceinline__ void lin_give_up(const LinArgs &A, int w) {
     const int bi = w >= 0 && w < A.work ? A.map.blob(w) : -1;
-    if (bi >= 0) set_status(A.state + (size_t)bi * A.L.blob, LQ_DEV_TIMEOUT);
+    if (bi < 0) return;
+    uint8_t *blob = A.state + (size_t)bi * A.L.blob;
+    if (A.cont || A.nseg > 1) set_status(blob, LQ_DEV_TIMEOUT);
+    else lin_new_header(blob, LQ_DEV_TIMEOUT);
 }
 
 template <int D>
@@ -124,7 +134,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             mbar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < kLpRing; ++i) {
-            ring[i].flags = kLpEnd;
+            ring[i].w = -1;
             mbar_init(&bars->ring_full[i], 1);
             mbar_init(&bars->ring_free[i], SH::SW + 17);  // output, key and score warps too
         }
@@ -140,6 +150,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             mbar_init(&bars->o_free[i], 4);
         }
         bars->chunks = 0xFFFFFFFFu;
+        bars->left[0] = bars->left[1] = -1;
         mbar_init(&bars->claim_done, 1);
         fence_mbar_init();
     }
@@ -152,7 +163,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const uint32_t tmem = bars->tmem;
     const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 
-    bool ok = true;  // false: a wait gave up; every role then leaves
+    bool ok = true;  // false: a wait gave up; the role then leaves
     auto wait = [&](uint64_t *b, uint32_t phase) {
         // the first try in line: most waits end there
         if (!mbar_try_wait(b, phase & 1u) && !mbar_wait_bounded(b, phase & 1u)) ok = false;
@@ -221,23 +232,21 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             const bool first_bad = t_begin < t_stop && !lin_gate_ok(first);
             if (t_begin >= t_stop || first_bad) {  // no chunk
                 LpSlot *sl = slot_wait();
-                if (lane == 0) {
+                if (ok && lane == 0) {
                     sl->w = w; sl->seg = seg; sl->t0 = t_begin; sl->n = 0; sl->zero_end = t_end;
                     sl->flags = kLpNone | kLpFirst | kLpLast | (holds_end || first_bad ? kLpFinal : 0) |
                                 (first_bad ? kLpBad : 0);
                 }
-                arrive(&bars->ring_full[r % kLpRing]);
+                if (ok) arrive(&bars->ring_full[r % kLpRing]);
                 ++r;
-                claimed();
-                continue;
             }
             const float *src = lin_state_source(A, w, seg, blob);
-            const bool from_zero = src == nullptr;
+            const bool from_zero = src == nullptr, some = t_begin < t_stop && !first_bad;
             // the state warps read it some chunks from now
-            if (src && lane == 0) bulk_prefetch_l2(src, D * D * 4);
+            if (some && src && lane == 0) bulk_prefetch_l2(src, D * D * 4);
             const int xq = (hh / A.group) * D, xv = hh * D, y0 = row * A.tokens;
 #pragma unroll 1
-            for (int t0 = t_begin; t0 < t_stop && ok;) {
+            for (int t0 = t_begin; some;) {
                 // the gates of the next chunk, if this one has all 64 tokens
                 const float n0 = gate(t0 + C + 2 * lane), n1 = gate(t0 + C + 2 * lane + 1), n64 = gate(t0 + 2 * C);
                 const unsigned w0 = __ballot_sync(0xFFFFFFFFu, !lin_gate_ok(a0));
@@ -275,7 +284,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                         tma_load_2d(sp + SH::V + kb * 8192, &mv, xv + 64 * kb, y0 + t0, &bars->full[st]);
                     }
                 }
+                ++c;
                 LpSlot *sl = slot_wait();
+                if (!ok) break;  // the slot is still in use
                 *reinterpret_cast<float2 *>(sl->G + 2 * lane) = make_float2(g0, g1);
                 *reinterpret_cast<float2 *>(sl->inv + 2 * lane) =
                     make_float2(2 * lane < n ? __fdiv_rn(1.f, g0) : 0.f, 2 * lane + 1 < n ? __fdiv_rn(1.f, g1) : 0.f);
@@ -288,7 +299,6 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 }
                 arrive(&bars->ring_full[r % kLpRing]);
                 ++r;
-                ++c;
                 t0 += n;
                 if (end) break;
                 if (n == C) {
@@ -298,25 +308,28 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 }
             }
             claimed();
-            if (!ok) {  // claimed, but not to be done
+            if (!ok) {
                 int nw = next >= 0 && next < A.work * A.nseg ? next / A.nseg : w;
                 if (ranked) nw = __shfl_sync(0xFFFFFFFFu, row_of_rank, nw / A.map.heads) * A.map.heads + nw % A.map.heads;
                 if (lane == 0) {
-                    lin_give_up(A, w);
-                    lin_give_up(A, nw);
+                    bars->left[0] = w;
+                    bars->left[1] = nw;
                 }
             }
         }
-        LpSlot *sl = slot_wait();
-        if (lane == 0) {
-            sl->flags = kLpEnd;
-            bars->chunks = c;
+        if (ok) {
+            LpSlot *sl = slot_wait();
+            if (ok && lane == 0) {
+                sl->w = -1;
+                sl->flags = kLpEnd;
+                bars->chunks = c;
+            }
+            if (ok) arrive(&bars->ring_full[r % kLpRing]);
         }
-        arrive(&bars->ring_full[r % kLpRing]);
         // what has been asked for lands before the CTA leaves
         for (uint32_t i = c >= ST ? c - ST : 0u; i < c; ++i) wait(&bars->full[i % ST], i / ST);
-        if (c >= ST) wait(&bars->empty[c % ST], c / ST - 1u);
-        arrive(&bars->full[c % ST]);  // warp 24 learns the end here
+        if (ok && c >= ST) wait(&bars->empty[c % ST], c / ST - 1u);
+        if (ok) arrive(&bars->full[c % ST]);  // warp 24 learns the end here
     } else if (warp == 18 || warp == 24) {
         // ------------------------------------------------------ the issuers
         constexpr uint32_t id64 = lc_idesc(128, 64, 0, 0), idpv = lc_idesc(128, 64, 1, 0),
@@ -424,15 +437,16 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const int kt = 32 * kw + lane;
         uint32_t c = 0;
 #pragma unroll 1
-        for (uint32_t r = 0; ok; ++r) {
+        for (uint32_t r = 0;; ++r) {
             wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            if (!ok) break;
             const LpSlot *sl = ring + r % kLpRing;
-            const int flags = ok ? sl->flags : kLpEnd;
+            const int flags = sl->flags;
             if (flags & (kLpEnd | kLpNone)) {
                 arrive(&bars->ring_free[r % kLpRing]);
                 if (flags & kLpEnd) {  // warp 18 learns it here
                     if (c >= NK) wait(&bars->d_done[c % NK], c / NK - 1u);
-                    arrive(&bars->k_ready[c % NK]);
+                    if (ok) arrive(&bars->k_ready[c % NK]);
                     break;
                 }
                 continue;
@@ -441,7 +455,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             uint8_t *sp = smem + (c % ST) * SH::STAGE;
             wait(&bars->full[c % ST], c / ST);
             if (c >= NK) wait(&bars->d_done[c % NK], c / NK - 1u);
-            if (ok) {
+            if (!ok) break;
+            {
                 // NT is a multiple of NP: a thread keeps its piece of the row
                 constexpr int RS = NT / NP, R = (C + RS - 1) / RS;
                 const int pc = kt % NP, t0 = kt / NP;
@@ -471,16 +486,18 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const int diag = warp == 17 ? 32 : lane;  // last column of the block that the row sees
         uint32_t c = 0;
 #pragma unroll 1
-        for (uint32_t r = 0; ok; ++r) {
+        for (uint32_t r = 0;; ++r) {
             wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            if (!ok) break;
             const LpSlot *sl = ring + r % kLpRing;
-            const int flags = ok ? sl->flags : kLpEnd;
+            const int flags = sl->flags;
             if (flags & (kLpEnd | kLpNone)) {
                 arrive(&bars->ring_free[r % kLpRing]);
                 if (flags & kLpEnd) break;
                 continue;
             }
             wait(&bars->qk_done, c);
+            if (!ok) break;
             tc_fence_after();
             uint32_t v[2][16];
             tmem_ld16_async(tlane + kLpQK + (uint32_t)c0, v[0]);
@@ -490,6 +507,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             tc_fence_before();
             arrive(&bars->qk_free);
             if (c > 0) wait(&bars->o_done[(c - 1u) & 1u], (c - 1u) / 2u);  // P is free
+            if (!ok) break;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -525,15 +543,17 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const uint32_t step = (uint32_t)A.map.heads * D;  // < 2^31
         uint32_t c = 0;
 #pragma unroll 1
-        for (uint32_t r = 0; ok; ++r) {
+        for (uint32_t r = 0;; ++r) {
             wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            if (!ok) break;
             const LpSlot *sl = ring + r % kLpRing;
-            const int flags = ok ? sl->flags : kLpEnd;
+            const int flags = sl->flags;
             if (flags & kLpEnd) break;
             const int row = sl->w / A.map.heads, hh = sl->w - row * A.map.heads, n = sl->n;
             if (!(flags & kLpNone)) {
                 float *o = A.out + lin_v_row(A, row, hh, sl->t0 + x0) * D + j;
                 wait(&bars->o_done[c & 1u], c / 2u);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int x = x0; x < x0 + TN; x += 32) {
@@ -557,7 +577,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                                     o[(uint64_t)(uint32_t)(y + z) * step] = __uint_as_float(v[(y + z) >> 4][(y + z) & 15]) * gg[z];
                         }
                     };
-                    if (A.out && ok) {
+                    if (A.out) {
                         if (n == C) put(32);
                         else put(n - x);
                     }
@@ -565,7 +585,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 }
                 ++c;
             }
-            if ((flags & kLpLast) && A.out && ok)  // no outputs past the prompt's end
+            if ((flags & kLpLast) && A.out)  // no outputs past the prompt's end
                 for (int x = ot; x < (sl->zero_end - sl->t0 - n) * (D / 4); x += NT)
                     *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, sl->t0 + n + x / (D / 4)) * D + 4 * (x % (D / 4))) =
                         make_float4(0.f, 0.f, 0.f, 0.f);
@@ -578,20 +598,20 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         uint32_t c = 0;
         float g = 1.f;  // scale of the accumulator
         bool from_zero = false;
-        int w = 0;
 #pragma unroll 1
-        for (uint32_t r = 0; ok; ++r) {
+        for (uint32_t r = 0;; ++r) {
             wait(&bars->ring_full[r % kLpRing], r / kLpRing);
+            if (!ok) break;
             const LpSlot *sl = ring + r % kLpRing;
-            const int flags = ok ? sl->flags : kLpEnd;
+            const int flags = sl->flags, w = sl->w;
             if (flags & kLpEnd) {
                 arrive(&bars->ring_free[r % kLpRing]);
                 break;
             }
-            w = sl->w;
             // S^T Q^T of the chunk before, and with it V^T K', which was issued before it
             if (c > 0) wait(&bars->y_done, c - 1u);
             if (c > 1) wait(&bars->o_free[c & 1u], c / 2u - 1u);  // for S^T Q^T of this chunk
+            if (!ok) break;
             tc_fence_after();
             if (flags & kLpFirst) {
                 const int bi = A.map.blob(w);
@@ -649,8 +669,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 g = sl->g_next;
                 ++c;
             }
-            if ((flags & kLpFinal) && ok) {  // the prompt's end
+            if (flags & kLpFinal) {  // the prompt's end
                 if (!(flags & kLpNone)) wait(&bars->y_done, c - 1u);
+                if (!ok) break;
                 tc_fence_after();
                 uint8_t *blob = A.state + (size_t)A.map.blob(w) * A.L.blob;
                 float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + (size_t)(HD * half) * D + j;
@@ -667,14 +688,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             }
             arrive(&bars->ring_free[r % kLpRing]);
         }
-        if (!ok && lane == 0) {  // the items that are described may not be done
-            lin_give_up(A, w);
-            for (int i = 0; i < kLpRing; ++i)
-                if (!(ring[i].flags & kLpEnd)) lin_give_up(A, ring[i].w);
-        }
     }
     tc_fence_before();
-    __syncthreads();
+    if (__syncthreads_or(!ok) && tid < kLpRing + 2) lin_give_up(A, tid < kLpRing ? ring[tid].w : bars->left[tid - kLpRing]);
     if (warp == 18) tmem_dealloc(tmem, 512u);
 }
 

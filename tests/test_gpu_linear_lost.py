@@ -54,8 +54,7 @@ def segments(st, work, need, d):
     return (need // 4 - work) // (work * (d * d + 2))
 
 
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("cont", [False, True])
+@pytest.mark.parametrize("cont,d", [(False, 64), (False, 128), (True, 128)])
 @pytest.mark.parametrize("name,nth", [("&bars->all_done", 0), ("&bars->d_done[i & 1]", 0),
                                       ("&bars->empty[i % kLsStages]", 1)])
 def test_a_lost_segment_is_reported(lossy, name, nth, cont, d):
@@ -90,3 +89,70 @@ def test_a_lost_segment_is_reported(lossy, name, nth, cont, d):
     near(out, want)
     near(st.dequant(), S)
     assert st.check() == 0
+
+
+QK, D_DONE, Y_DONE, O_DONE, EMPTY = ("&bars->qk_done", "&bars->d_done[c % NK]", "&bars->y_done", "&bars->o_done[c & 1u]",
+                                     "&bars->empty[st]")
+
+
+def check_heads(st, out, want, S, n, h, d):
+    """Every head is right or has LQ_DEV_TIMEOUT; returns how many have it."""
+    state = st.blobs()[:, 128:128 + 4 * d * d].contiguous().view(torch.float32).view(n, h, d, d)
+    status = st.blobs()[:, 4:8].contiguous().view(torch.int32).view(n, h)
+    assert ((status == 0) | (status == TIMEOUT)).all()
+    good = status == 0
+    near(out.transpose(1, 2)[good], want.transpose(1, 2)[good], "outputs of the other heads")
+    near(state[good], S[good], "states of the other heads")
+    assert (st.blobs()[:, 12:16].contiguous().view(torch.int32) == 0x4C515354).all()
+    return int((~good).sum())
+
+
+@pytest.mark.parametrize("cont,d", [(False, 64), (False, 128), (True, 128)])
+@pytest.mark.parametrize("name,n,h,t,nth", [
+    # many heads: one SM takes several, one after the other
+    (QK, 50, 12, 130, 4), (D_DONE, 50, 12, 130, 4), (Y_DONE, 50, 12, 130, 4), (O_DONE, 50, 12, 130, 4), (EMPTY, 50, 12, 130, 4),
+    (O_DONE, 50, 12, 130, 0),
+    # one head, the last of its chunks: its state is complete where its outputs are not
+    (QK, 1, 1, 200, 3), (Y_DONE, 1, 1, 200, 3), (O_DONE, 1, 1, 200, 3)])
+def test_lost_chunks_are_reported(lossy, name, n, h, t, nth, cont, d):
+    """A chunk whose products are not seen to end: whatever it leaves unfinished
+    has the status, whichever role gave up."""
+    x = inputs(81, n, t, h, h, d, torch.bfloat16)
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, torch.bfloat16)
+    if cont:
+        st.init(x["S0"])
+    out = torch.full_like(want, float("nan"), dtype=torch.float32)
+    call = dict(tokens=t, q=x["q"], k=x["k"], v=x["v"], decay=x["decay"], out=out)
+    assert lossy(name, nth=nth) == 0
+    st.linear_prefill(**call, S0=None if cont else x["S0"], cont=cont)
+    torch.cuda.synchronize()
+    # at most the described ones, the one being fed and the one claimed
+    assert 1 <= check_heads(st, out, want, S, n, h, d) <= 6
+    assert lossy("") == 0
+    st.linear_prefill(**call, S0=x["S0"])
+    assert check_heads(st, out, want, S, n, h, d) == 0
+
+
+@pytest.mark.parametrize("cont,d", [(False, 64), (False, 128), (True, 128)])
+def test_a_chunk_lost_in_a_segment_is_reported(lossy, cont, d):
+    """A prompt cut along time: the segment that loses a chunk is not the one that
+    holds the prompt's end, whose CTA goes on."""
+    from linear_attention_recurrent_lq_b200 import binding as b
+    n, h, t = 1, 24, 2500
+    x = inputs(82, n, t, h, h, d, torch.bfloat16)
+    want, S = reference(x, x["S0"])
+    st = state_of(n, h, d, torch.bfloat16)
+    if cont:
+        st.init(x["S0"])
+    nseg = segments(st, n * h, b.lq_linear_prefill_workspace(st.cfg, n, t), d)
+    out = torch.full_like(want, float("nan"), dtype=torch.float32)
+    call = dict(tokens=t, q=x["q"], k=x["k"], v=x["v"], decay=x["decay"], out=out)
+    assert lossy(O_DONE, block=nseg + 1) == 0   # the second segment of the second head
+    st.linear_prefill(**call, S0=None if cont else x["S0"], cont=cont)
+    torch.cuda.synchronize()
+    assert st.blobs()[1, 4:8].view(torch.int32).item() == TIMEOUT
+    assert 1 <= check_heads(st, out, want, S, n, h, d) <= 6
+    assert lossy("") == 0
+    st.linear_prefill(**call, S0=x["S0"])
+    assert check_heads(st, out, want, S, n, h, d) == 0
