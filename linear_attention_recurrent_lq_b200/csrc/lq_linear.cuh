@@ -65,6 +65,14 @@ __device__ __forceinline__ int lin_last_segment(const LinArgs &A, int len) {
     return len > 0 ? (len - 1) / A.seg_len : 0;
 }
 
+// Where the tokens that a segment [t_begin, t_end) takes in end: at its start
+// if it does not run or lies behind the prompt.  From there to t_end its outputs
+// are zeros, so the segments of a row write each output once.
+__host__ __device__ __forceinline__ int lin_stop(bool run, int len, int t_begin, int t_end) {
+    const int t = len < t_end ? len : t_end;
+    return run && t > t_begin ? t : t_begin;
+}
+
 // Where work item w's segment starts from; null: a zero state.
 __device__ __forceinline__ const float *lin_state_source(const LinArgs &A, int w, int seg, const uint8_t *blob) {
     const size_t n = A.L.pairs_off - A.L.qs_off;  // bytes of a state
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(kLinThreads, C == 8 ? 2 : 4) lin_recurrent_ker
             asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     }
     const int t_begin = seg * A.seg_len, t_end = min(A.tokens, t_begin + A.seg_len);
-    const int t_stop = run ? min(len, t_end) : t_begin;
+    const int t_stop = lin_stop(run, len, t_begin, t_end);
 
     // ---- the state this segment starts from
     float2 S[2 * M][C];

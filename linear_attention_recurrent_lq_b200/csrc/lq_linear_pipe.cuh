@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 run = !__any_sync(0xFFFFFFFFu, stop);
             }
             const int t_begin = seg * A.seg_len, t_end = min(A.tokens, t_begin + A.seg_len);
-            const int t_stop = run ? min(len, t_end) : t_begin;
+            const int t_stop = lin_stop(run, len, t_begin, t_end);
             const bool holds_end = run && seg == last;
             const float *gates = A.decay + lin_v_row(A, row, hh, 0);
             const size_t gs = (size_t)A.map.heads;
