@@ -481,9 +481,9 @@ __global__ void __launch_bounds__(kLinThreads, C == 8 ? 2 : 4) lin_recurrent_ker
         }
         return;
     }
-    if (A.out)  // no outputs past the prompt's end
-        for (int x = tid; x < (t_end - t_done) * SH::COLS; x += kLinThreads)
-            A.out[lin_v_row(A, row, hh, t_done + x / SH::COLS) * D + jc + x % SH::COLS] = 0.f;
+    if (A.out)  // no outputs past the prompt's end (tokens x columns may pass 2^31)
+        for (int t = t_done + tid / SH::COLS; t < t_end; t += kLinThreads / SH::COLS)
+            A.out[lin_v_row(A, row, hh, t) * D + jc + tid % SH::COLS] = 0.f;
     if (run && (bad != kNoBad || seg == last)) {  // this segment holds the prompt's end
         float *dst = reinterpret_cast<float *>(blob + kHdrBytes) + jc + jt;
 #pragma unroll

@@ -585,9 +585,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 }
                 ++c;
             }
-            if ((flags & kLpLast) && A.out)  // no outputs past the prompt's end
-                for (int x = ot; x < (sl->zero_end - sl->t0 - n) * (D / 4); x += NT)
-                    *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, sl->t0 + n + x / (D / 4)) * D + 4 * (x % (D / 4))) =
+            if ((flags & kLpLast) && A.out)  // no outputs past the prompt's end (tokens x columns may pass 2^31)
+                for (int t = sl->t0 + n + ot / (D / 4), end = sl->zero_end; t < end; t += NT / (D / 4))
+                    *reinterpret_cast<float4 *>(A.out + lin_v_row(A, row, hh, t) * D + 4 * (ot % (D / 4))) =
                         make_float4(0.f, 0.f, 0.f, 0.f);
             arrive(&bars->ring_free[r % kLpRing]);
         }
