@@ -346,7 +346,7 @@ LQ_API lq_status lq_copy_slots(const lq_config *cfg, void *dst, int dst_num_slot
  * lq_check_status work on the same buffers.
  *   qk_heads  Hk: queries and keys have Hk heads, H % Hk == 0, and value head
  *             h reads query / key head h / (H / Hk)
- *   decay     a, in [0, 1]; a negative, infinite or NaN gate sets LQ_DEV_RANGE
+ *   decay     a, in [0, 1]; any other value, NaN too, sets LQ_DEV_RANGE
  * Alignment: q, k, v, S0, out and workspace 16 bytes, decay, slots and
  * lengths 4.  A non-finite q, k or v makes its head's state non-finite, as
  * the formula has it; in a prompt it may also reach outputs of the same head

@@ -13,8 +13,6 @@
 // head h reads query / key head h / (H / Hk).
 #pragma once
 
-#include <float.h>
-
 #include "lq_common.cuh"
 
 namespace lq {
@@ -46,7 +44,9 @@ struct LinArgs {
 constexpr int kNoBad = 0x7FFFFFFF;  // no gate is bad
 constexpr int kLost = -1;           // a wait of the first pass gave up: the segment's state is not there
 
-__device__ __forceinline__ bool lin_gate_ok(float a) { return a >= 0.f && a <= FLT_MAX; }
+// The forms of a prompt divide by products of gates, which must not grow past
+// FP32's range: a gate above 1 is as wrong as a negative one.
+__device__ __forceinline__ bool lin_gate_ok(float a) { return a >= 0.f && a <= 1.f; }
 
 // Row indices of token t of work item (row, hh).
 __device__ __forceinline__ size_t lin_v_row(const LinArgs &A, int row, int hh, int t) {
