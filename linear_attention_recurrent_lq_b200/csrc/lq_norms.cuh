@@ -67,9 +67,22 @@ __device__ __forceinline__ float2 gate_decay2(float2 x, float rate) {
     return make_float2(__expf(t.x), __expf(t.y));
 }
 
-__device__ __forceinline__ float sigmoidf(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
-// the same within 1e-6: an output gate is rounded with y once more
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + exp(-x)) from e = exp(-|x|), which never overflows: e / (1 + e) below
+// zero, so that a gate far below keeps its digits down to FP32's smallest values.
+__device__ __forceinline__ float sigmoidf(float x) {
+    const float e = expf(-fabsf(x));
+    return __fdiv_rn(x < 0.f ? e : 1.f, 1.f + e);
+}
+// The same for a result that is rounded to bf16 (2^-8) next, from 2^24 e: the
+// exponent -|x| log2(e) + 24 is rounded by at most 2^-18, so the result is within
+// 1e-5, and nothing is flushed to zero before x = -104, where a silu is below
+// bf16's smallest value.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(-fabsf(x), 1.44269504f, 24.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 0x1p24f));
+    return (x < 0.f ? e : 0x1p24f) * r;
+}
 
 template <bool BF16>
 __device__ __forceinline__ void unpack_piece(const uint4 &w, float (&x)[BF16 ? 8 : 4]) {
@@ -240,8 +253,10 @@ __global__ void __launch_bounds__(256) out_norm_kernel(OutNormArgs A) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float y = x[u][i] * f * w[i];
-            if constexpr (GATE == kGateSilu) y *= g[u][i] * sigmoid_fast(g[u][i]);
-            if constexpr (GATE == kGateSigmoid) y *= sigmoid_fast(g[u][i]);
+            if constexpr (GATE != kGateNone) {
+                const float sg = BF16 ? sigmoid_fast(g[u][i]) : sigmoidf(g[u][i]);
+                y *= GATE == kGateSilu ? g[u][i] * sg : sg;
+            }
             x[u][i] = y;
         }
         const long long r = r0 + u * G;
