@@ -294,7 +294,7 @@ template <int D, bool BF16>
 cudaError_t launch_qk_norm(QkNormArgs a, cudaStream_t s) {
     constexpr int G = 256 / (D / (BF16 ? 8 : 4));  // rows a block takes at once
     const long long nb = (2 * a.qk_rows + G * kNormUnroll - 1) / (G * kNormUnroll);
-    const long long per = a.kda ? G * kGateUnroll : 256, ng = (a.heads_n + per - 1) / per;
+    const long long per = a.kda ? G * kGateUnroll<BF16> : 256, ng = (a.heads_n + per - 1) / per;
     if (nb + ng > 0x7FFFFFFF) return cudaErrorInvalidValue;
     a.norm_blocks = (unsigned)nb;
     a.gate_blocks = (unsigned)ng;

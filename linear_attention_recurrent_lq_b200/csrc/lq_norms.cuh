@@ -47,24 +47,66 @@ __device__ __forceinline__ void store_piece(void *p, const float (&x)[BF16 ? 8 :
     *reinterpret_cast<uint4 *>(p) = w;
 }
 
-// exp(-rate softplus(x)) of two, softplus(x) = max(x, 0) + log(1 + e), e =
-// exp(-|x|).  Small ones have to keep their digits, so log(1 + e) is not taken of
-// a rounded 1 + e but from its series 2 artanh(r), r = e / (2 + e) <= 1/3; the
-// first term left out is r^14 / 15 <= 1.4e-8 of the sum.  With log1pf and expf
-// the gates of a key-channel layer took as long as its memory traffic twice.
-__device__ __forceinline__ float2 gate_decay2(float2 x, float rate) {
-    const float2 e = make_float2(__expf(-fabsf(x.x)), __expf(-fabsf(x.y)));
-    const float2 r = make_float2(__fdividef(e.x, 2.f + e.x), __fdividef(e.y, 2.f + e.y)), r2 = __fmul2_rn(r, r);
+// 2^x and 1 / x within 2 and 1 units of 2^-23; results below FP32's normal numbers
+// are zeros.
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596303e-8f;  // log2(e), and what its rounding left
+constexpr float kLn2 = 0.693147181f;
+
+// -rate log2(e) in two floats, rate = exp(a_log).
+struct GateRate {
+    float hi, lo;
+    __device__ __forceinline__ explicit GateRate(float a_log) {
+        const float y = a_log * kLog2e, z = ex2_ftz(y);
+        const float rate = fmaf(z, kLn2 * fmaf(a_log, kLog2eRest, fmaf(a_log, kLog2e, -y)), z);
+        hi = -rate * kLog2e;
+        lo = fmaf(-rate, kLog2eRest, fmaf(-rate, kLog2e, -hi));
+    }
+    // times a softplus up to 2^63 it stays inside FP32, and the decay is 0 there
+    __device__ __forceinline__ bool usual() const { return hi <= -0x1p-55f && hi >= -0x1p63f; }
+};
+
+// exp(-exp(a_log) softplus(x)) for rates outside GateRate's usual range.
+__device__ __noinline__ float gate_decay_far(float x, float a_log) {
+    return expf(-expf(a_log) * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)))));
+}
+
+// exp(-rate softplus(x)) of two for a usual rate, softplus(x) = max(x, 0) +
+// log(1 + e), e = exp(-|x|).  Small ones have to keep their digits, so log(1 + e) is
+// not taken of a rounded 1 + e but as 2 artanh(r), r = e / (2 + e) <= 1/3, r times a
+// polynomial in r^2 (least maximum of the relative error, 5e-9).  e is within
+// (4 + 2.4 |x|) units of 2^-24, of the order of what the rounded sum a + dt_bias
+// does to it (|x| units).  The exponent of the result may be large, so the rounding
+// error of the product rate times softplus, a unit for each unit of the exponent,
+// is kept and put back: the result is as exact as its two factors are.
+__device__ __forceinline__ float2 gate_decay2(float2 x, const GateRate &rate) {
     auto both = [](float c) { return make_float2(c, c); };
-    float2 p = __ffma2_rn(r2, both(1.f / 13.f), both(1.f / 11.f));
-    p = __ffma2_rn(r2, p, both(1.f / 9.f));
-    p = __ffma2_rn(r2, p, both(1.f / 7.f));
-    p = __ffma2_rn(r2, p, both(1.f / 5.f));
-    p = __ffma2_rn(r2, p, both(1.f / 3.f));
-    p = __ffma2_rn(r2, p, both(1.f));
-    const float2 soft = __ffma2_rn(__fmul2_rn(both(2.f), r), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
-    const float2 t = __fmul2_rn(both(-rate), soft);
-    return make_float2(__expf(t.x), __expf(t.y));
+    const float2 e = make_float2(ex2_ftz(-kLog2e * fabsf(x.x)), ex2_ftz(-kLog2e * fabsf(x.y)));
+    const float2 e2 = __fadd2_rn(e, both(2.f));
+    const float2 r = __fmul2_rn(e, make_float2(rcp_ftz(e2.x), rcp_ftz(e2.y))), r2 = __fmul2_rn(r, r);
+    float2 p = __ffma2_rn(r2, both(0.280244589f), both(0.279991418f));
+    p = __ffma2_rn(r2, p, both(0.400216997f));
+    p = __ffma2_rn(r2, p, both(0.666664124f));
+    p = __ffma2_rn(r2, p, both(2.f));
+    // beyond 2^63 the decay is 0, as it is at 2^63
+    const float2 soft = __ffma2_rn(r, p, make_float2(fminf(fmaxf(x.x, 0.f), 0x1p63f), fminf(fmaxf(x.y, 0.f), 0x1p63f)));
+    const float2 y = __fmul2_rn(both(rate.hi), soft);
+    float2 left = __ffma2_rn(both(rate.hi), soft, make_float2(-y.x, -y.y));
+    left = __fmul2_rn(both(kLn2), __ffma2_rn(both(rate.lo), soft, left));
+    float2 z;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(z.x) : "f"(y.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(z.y) : "f"(y.y));
+    return __ffma2_rn(z, left, z);
 }
 
 // 1 / (1 + exp(-x)) from e = exp(-|x|), which never overflows: e / (1 + e) below
@@ -78,10 +120,8 @@ __device__ __forceinline__ float sigmoidf(float x) {
 // 1e-5, and nothing is flushed to zero before x = -104, where a silu is below
 // bf16's smallest value.
 __device__ __forceinline__ float sigmoid_fast(float x) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(-fabsf(x), 1.44269504f, 24.f)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 0x1p24f));
-    return (x < 0.f ? e : 0x1p24f) * r;
+    const float e = ex2_ftz(fmaf(-fabsf(x), kLog2e, 24.f));
+    return (x < 0.f ? e : 0x1p24f) * rcp_ftz(e + 0x1p24f);
 }
 
 template <bool BF16>
@@ -99,9 +139,11 @@ __device__ __forceinline__ void unpack_piece(const uint4 &w, float (&x)[BF16 ? 8
 }
 
 // Pieces of 16 bytes a thread loads before it uses the first: 8 for q and k
-// rows, 4 for the gates of key channels (4 and 1: 95 us for 16384 tokens of 12
-// heads, d = 128, 54 us of memory traffic).
-constexpr int kNormUnroll = 8, kGateUnroll = 4;
+// rows, 32 values for the gates of key channels (16384 tokens of 12 heads, d = 128,
+// bf16: 2, 4 and 8 pieces 76.7, 71.6 and 91.4 us; f32: 130, 118 and 111 us).
+constexpr int kNormUnroll = 8;
+template <bool BF16>
+constexpr int kGateUnroll = BF16 ? 4 : 8;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) qk_norm_kernel(QkNormArgs A) {
@@ -147,27 +189,38 @@ __global__ void __launch_bounds__(256) qk_norm_kernel(QkNormArgs A) {
         return;
     }
     if (A.kda) {  // V channels of one head
-        const unsigned r0 = gates * (G * kGateUnroll) + tid / LR;  // rows * H < 2^31
+        const unsigned r0 = gates * (G * kGateUnroll<BF16>) + tid / LR;  // rows * H < 2^31
         // heads of the rows u G apart: one division, then steps
         unsigned h = r0 % (unsigned)A.H;
         const unsigned step = G % (unsigned)A.H;
-        uint4 w[kGateUnroll];
+        uint4 w[kGateUnroll<BF16>];
+        float a_log[kGateUnroll<BF16>];
 #pragma unroll
-        for (int u = 0; u < kGateUnroll; ++u) {
+        for (int u = 0; u < kGateUnroll<BF16>; ++u) {
             const unsigned r = r0 + u * G;
+            a_log[u] = __ldg(A.a_log + h);
+            h += step;
+            if (h >= (unsigned)A.H) h -= (unsigned)A.H;
             w[u] = r < A.heads_n ? __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.a) + ((size_t)r * D + c) * E))
                                  : make_uint4(0u, 0u, 0u, 0u);
         }
+        h = r0 % (unsigned)A.H;
 #pragma unroll
-        for (int u = 0; u < kGateUnroll; ++u) {
+        for (int u = 0; u < kGateUnroll<BF16>; ++u) {
             const unsigned r = r0 + u * G;
             if (r >= A.heads_n) return;
-            const float rate = __expf(A.a_log[h]);
+            const GateRate rate(a_log[u]);
             float x[V];
             unpack_piece<BF16>(w[u], x);
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
                 const float4 d = __ldg(reinterpret_cast<const float4 *>(A.dt_bias + (size_t)h * D + c + i));
+                if (!rate.usual()) {
+                    *reinterpret_cast<float4 *>(A.decay + (size_t)r * D + c + i) =
+                        make_float4(gate_decay_far(x[i] + d.x, a_log[u]), gate_decay_far(x[i + 1] + d.y, a_log[u]),
+                                    gate_decay_far(x[i + 2] + d.z, a_log[u]), gate_decay_far(x[i + 3] + d.w, a_log[u]));
+                    continue;
+                }
                 const float2 g0 = gate_decay2(__fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(d.x, d.y)), rate);
                 const float2 g1 = gate_decay2(__fadd2_rn(make_float2(x[i + 2], x[i + 3]), make_float2(d.z, d.w)), rate);
                 *reinterpret_cast<float4 *>(A.decay + (size_t)r * D + c + i) = make_float4(g0.x, g0.y, g1.x, g1.y);
@@ -182,7 +235,9 @@ __global__ void __launch_bounds__(256) qk_norm_kernel(QkNormArgs A) {
     if (x >= A.heads_n) return;
     const unsigned h = x % (unsigned)A.H;
     const float z = load_in(A.a, (size_t)x, BF16) + A.dt_bias[h];
-    A.decay[x] = gate_decay2(make_float2(z, z), expf(A.a_log[h])).x;
+    const float a_log = A.a_log[h];
+    const GateRate rate(a_log);
+    A.decay[x] = rate.usual() ? gate_decay2(make_float2(z, z), rate).x : gate_decay_far(z, a_log);
     A.beta[x] = sigmoidf(load_in(A.b, (size_t)x, BF16));
 }
 
