@@ -61,13 +61,7 @@ class HostIOPipeline:
         self.flush = flush
         for lay in layers:
             if lay.proj is not None:
-                x, c = lay.dev_in, lay.state.cfg
-                heads = (*x["v"].shape[:-1],)  # [W, rows, H]
-                f32 = dict(dtype=torch.float32, device=x["v"].device)
-                lay.scratch = dict(q=torch.empty_like(x["q"]), k=torch.empty_like(x["k"]), v=x["v"],
-                                   beta=torch.empty(heads, **f32),
-                                   decay=torch.empty(heads + ((c.dk,) if c.decay_kind == 1 else ()), **f32),
-                                   rows=torch.empty(x["v"].shape, **f32))
+                self._make_scratch(lay)
         self.up = torch.cuda.Stream()
         self.comp = torch.cuda.Stream()
         self.down = torch.cuda.Stream()
@@ -75,6 +69,24 @@ class HostIOPipeline:
         self.up_done = [torch.cuda.Event() for _ in range(n)]
         self.comp_done = [torch.cuda.Event() for _ in range(n)]
         self.down_done = [torch.cuda.Event() for _ in range(n)]
+
+    def _make_scratch(self, lay: Layer):
+        """The layer's scratch tensors.  They belong to the layer, as a graph that
+        was captured from it holds their addresses: another pipeline over the layer
+        uses the same ones, and a graph whose scratch no longer fits is dropped."""
+        torch = self.torch
+        x, c = lay.dev_in, lay.state.cfg
+        heads = (*x["v"].shape[:-1],)  # [W, rows, H]
+        want = dict(q=(x["q"].shape, x["q"].dtype), k=(x["k"].shape, x["k"].dtype), beta=(heads, torch.float32),
+                    decay=(heads + ((c.dk,) if c.decay_kind == 1 else ()), torch.float32),
+                    rows=(x["v"].shape, torch.float32))
+        dev, have = x["v"].device, lay.scratch
+        if have is not None and all(n in have and have[n].device == dev and have[n].dtype == t
+                                    and tuple(have[n].shape) == tuple(s) for n, (s, t) in want.items()):
+            have["v"] = x["v"]
+            return
+        lay.graph = None
+        lay.scratch = dict({n: torch.empty(tuple(s), dtype=t, device=dev) for n, (s, t) in want.items()}, v=x["v"])
 
     def _window(self, lay: Layer):
         x, p, rows = lay.dev_in, lay.proj, lay.dev_out
