@@ -3,6 +3,7 @@ in place, next to this file."""
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import re
 import subprocess
@@ -29,8 +30,17 @@ def _deps():
             + [os.path.join(ROOT, "include", "leapquant.h")])
 
 
-def needs_build() -> bool:
-    if not os.path.exists(LIB):
+def _built_with():
+    """The additional flags the library was built with (none, where nothing says so)."""
+    path = os.path.join(OBJ, "extra_flags")
+    if not os.path.exists(path):
+        return []
+    with open(path) as f:
+        return f.read().split("\n")[:-1]
+
+
+def needs_build(extra=()) -> bool:
+    if not os.path.exists(LIB) or _built_with() != list(extra):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(p) > t for p in _deps())
@@ -50,16 +60,19 @@ def _headers_of(src):
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile each source to an object (only those older than what they
-    include, at once) and link them into libleapquant.so."""
-    if not force and not needs_build():
+    include, at once) and link them into libleapquant.so.  `extra`: more compiler
+    flags; objects built with some are kept apart from those built without."""
+    extra = list(extra)
+    if not force and not needs_build(extra):
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
-    os.makedirs(OBJ, exist_ok=True)
+    obj_dir = OBJ if not extra else os.path.join(OBJ, hashlib.sha256("\n".join(extra).encode()).hexdigest()[:16])
+    os.makedirs(obj_dir, exist_ok=True)
     jobs, objs = [], []
     for src in _sources():
-        obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
+        obj = os.path.join(obj_dir, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
-        if not force and not extra and os.path.exists(obj):
+        if not force and os.path.exists(obj):
             t = os.path.getmtime(obj)
             if all(os.path.getmtime(p) <= t for p in [src, *_headers_of(src)]):
                 continue
@@ -75,6 +88,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     cmd = [nvcc, *NVCC_FLAGS, "-shared", "-o", LIB + ".tmp", *objs]
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+    with open(os.path.join(OBJ, "extra_flags"), "w") as f:
+        f.writelines(x + "\n" for x in extra)
     return LIB
 
 
