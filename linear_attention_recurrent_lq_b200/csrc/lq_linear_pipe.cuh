@@ -165,8 +165,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 
     bool ok = true;  // false: a wait gave up; the role then leaves
     auto wait = [&](uint64_t *b, uint32_t phase) {
-        // the first try in line: most waits end there
-        if (!mbar_try_wait(b, phase & 1u) && !mbar_wait_bounded(b, phase & 1u)) ok = false;
+        // the first try in line: most waits end there.  The outcome is the warp's: a
+        // phase may end between two lanes' last looks at it, and tensor memory is read
+        // and written by whole warps only
+        const bool got = mbar_try_wait(b, phase & 1u) || mbar_wait_bounded(b, phase & 1u);
+        ok = __all_sync(0xFFFFFFFFu, got) && ok;
     };
     auto arrive = [&](uint64_t *b) {  // one arrival per warp, after all its lanes
         __syncwarp();

@@ -82,8 +82,9 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     const uint32_t tmem = bars->tmem;
     const int t_begin = seg * A.seg_len, chunks = A.seg_len / C;
     bool ok = true;
-    auto wait = [&](uint64_t *b, uint32_t phase) {
-        if (!mbar_try_wait(b, phase & 1u) && !mbar_wait_bounded(b, phase & 1u)) ok = false;
+    auto wait = [&](uint64_t *b, uint32_t phase) {  // the outcome is the warp's
+        const bool got = mbar_try_wait(b, phase & 1u) || mbar_wait_bounded(b, phase & 1u);
+        ok = __all_sync(0xFFFFFFFFu, got) && ok;
     };
 
     if (warp == kLsKeys + 2) {  // the loads

@@ -31,3 +31,13 @@ def test_the_loading_warp_waits_for_all_its_loads(name):
     tail = text[text.rindex("tma_load_2d("):]
     loop = re.search(r"for \((?:uint32_t|int) (\w) = (\w) >=? (\w+) \? \2 - \3 : 0u?; \1 < \2; \+\+\1\)\s*wait\(&bars->full\[", tail)
     assert loop and loop.group(3) in ("ST", "kLsStages")
+
+
+@pytest.mark.parametrize("name", ["lq_linear_pipe.cuh", "lq_linear_state.cuh"])
+def test_a_wait_that_gives_up_does_so_for_its_whole_warp(name):
+    """Behind a wait stand instructions of whole warps (tensor memory, shuffles): the
+    lanes agree on its outcome, also where the phase ends as the first ones give up."""
+    text = open(os.path.join(CSRC, name)).read()
+    body = re.search(r"auto wait = \[&\]\(uint64_t \*b, uint32_t phase\) \{(.*?)\n    \};", text, flags=re.S).group(1)
+    assert re.search(r"ok = __all_sync\(0xFFFFFFFFu, got\) && ok;", body)
+    assert "ok = false" not in text
