@@ -348,10 +348,11 @@ LQ_API lq_status lq_copy_slots(const lq_config *cfg, void *dst, int dst_num_slot
  *             h reads query / key head h / (H / Hk)
  *   decay     a, in [0, 1]; any other value, NaN too, sets LQ_DEV_RANGE
  * Alignment: q, k, v, S0, out and workspace 16 bytes, decay, slots and
- * lengths 4.  A non-finite q, k or v makes its head's state non-finite, as
- * the formula has it; in a prompt it may also reach outputs of the same head
- * up to 63 tokens before it.  Prompts hold the state over a product of gates of
- * 2^-64 or more, so a state or k v^T beyond 2^63 may overflow there. */
+ * lengths 4.  A non-finite k or v makes its head's state non-finite, as the
+ * formula has it, and a non-finite q its token's outputs; in a prompt a
+ * non-finite v may also reach outputs of the same head up to 63 tokens before
+ * it.  Prompts hold the state over a product of gates of 2^-64 or more, so a
+ * k, a v, a state, or products k v^T and q^T k beyond 2^63 may overflow there. */
 
 /* One token for every (slot, head).
  *   q, k [N, Hk, dk]  v [N, H, dv] in_dtype   decay [N, H]   out [N, H, dv] f32
@@ -374,7 +375,8 @@ LQ_API size_t lq_linear_prefill_workspace(const lq_config *cfg, int rows, int to
 /* A prompt for every (slot, head).
  *   tokens   T >= 0
  *   lengths  [N] int32, device, or NULL: row n's prompt is its first
- *            clamp(lengths[n], 0, T) tokens; what lies behind is not read
+ *            clamp(lengths[n], 0, T) tokens; what lies behind may be read, but
+ *            has no effect whatever it holds
  *   S0       [N, H, dk, dv] f32 or NULL (zero state)
  *   q, k     [N, T, Hk, dk]  v [N, T, H, dv] in_dtype   decay [N, T, H] f32
  *   out      [N, T, H, dv] f32 or NULL; zero past a row's length

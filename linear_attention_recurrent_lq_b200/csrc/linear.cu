@@ -15,6 +15,8 @@ using namespace lq;
 
 namespace {
 
+// The choices below were measured on a B200 and count its SMs; on a part with
+// another number they would cost time, not results.
 constexpr int kSms = 148;
 
 // Token after token, a CTA takes 16, 64 or (d = 128) 128 columns of a head.
@@ -104,7 +106,9 @@ Cut cut_of(const lq_config &c, int64_t work, int tokens) {
     int64_t n;
     if (c.dv == 64) {
         if (work * tokens >= 133 * (int64_t)tokens - 14000) return best;
-        n = 6 * kSms / work;  // CTAs per SM: 36 heads of 777 tokens 36 us, with three 47 us
+        // CTAs per SM: 36 heads of 777 tokens 36 us, with three 47 us.  Not the best
+        // everywhere: 36 heads of 400 tokens 33 us (segments of 48), 27 in segments of 32
+        n = 6 * kSms / work;
     } else {
         if (work * tokens >= 84 * (int64_t)tokens - 11500) return best;
         // CTAs of 128 columns two per SM, or twice as many: 36 heads of 2000 tokens

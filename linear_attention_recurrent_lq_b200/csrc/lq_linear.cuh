@@ -9,8 +9,8 @@
 // Kernels here: one token (lin_step_kernel), a prompt token after token
 // (lin_recurrent_kernel, also the first pass of a prompt cut along time), and
 // the pass that joins the cuts (lin_scan_kernel).  The chunkwise form on the
-// tensor cores is in lq_linear_pipe.cuh and lq_linear_state.cuh.  Grouped queries and keys: value
-// head h reads query / key head h / (H / Hk).
+// tensor cores is in lq_linear_pipe.cuh and lq_linear_state.cuh.  Grouped queries
+// and keys: value head h reads query / key head h / (H / Hk).
 #pragma once
 
 #include "lq_common.cuh"
@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(256, 3) lin_step_kernel(LinArgs A) {
 // 16 tokens whose gates multiply to less than 2^-48 (gates of 0 among them)
 // are taken one by one from G = 1: S = a_t S + k_t v_t^T.  f32, 2048 heads of 256
 // tokens: d = 128 833 us, 462 of them multiply-adds at their peak rate; d = 64
-// 266 us (115); the rest are reads of q, k and v from shared memory.
+// 266 us (115); the rest are reads of q, k and v from shared memory.  Of 64 columns,
+// f32 and d = 128, the kernel fills its 128 registers and spills 84 bytes.
 constexpr int kLinTokens = 16;  // tokens per stage
 constexpr int kLinStages = 3;
 constexpr int kLinThreads = 128;

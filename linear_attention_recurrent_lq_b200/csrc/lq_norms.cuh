@@ -8,8 +8,9 @@
 // Both are bound by HBM: each value is read once with 16-byte loads, several
 // rows in flight per thread, sums and gates in FP32, one rounding at the end.
 // Measured, bf16, d = 128: qk_norm of 16384 tokens of 12 heads with a gate per key
-// channel 73.0 us (54.0 at the copy's rate; bound by instruction issue), out_norm of
-// 16384 tokens of 32 heads 90.6 us, 5930 GB/s (82.0).
+// channel 74 us (54.0 at the copy's rate; the latency of the gates' exponentials, with
+// a third of the warps that an SM holds), out_norm of 16384 tokens of 32 heads 92 us,
+// 5840 GB/s (82.0).
 #pragma once
 
 #include "lq_linear.cuh"

@@ -28,7 +28,7 @@ def lossy(tmp_path_factory):
     build.build()
     from linear_attention_recurrent_lq_b200 import binding as b
     out = str(tmp_path_factory.mktemp("lossy") / "lossy.so")
-    subprocess.run(["nvcc", *build.NVCC_FLAGS, "-shared", "-I", os.path.join(ROOT, "include"), "-I",
+    subprocess.run([os.environ.get("NVCC", "nvcc"), *build.NVCC_FLAGS, "-shared", "-I", os.path.join(ROOT, "include"), "-I",
                     os.path.join(build.HERE, "csrc"), "-o", out, os.path.join(ROOT, "tests", "lost_commit.cu")], check=True)
     so = ctypes.CDLL(out)
     for name in ("lq_linear_prefill", "lq_linear_prefill_workspace"):
