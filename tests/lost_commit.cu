@@ -1,7 +1,13 @@
 // The linear-attention entry points with one arrival left out: a chosen
-// tcgen05.commit of one CTA is not made, so that what waits for it runs into its
-// time limit.  Every wait is bounded and every CTA waits, bounded too, for what it
-// has in flight before it leaves.
+// tcgen05.commit of one CTA is not made, a flag that nothing sets, so that what waits
+// for it runs into its limit of a second and the status is seen.  Nothing else
+// changes, so every access is one that the whole kernel makes: a role that gives up
+// leaves before it reads or writes anything behind the wait, without an arrival, so
+// no other role goes on to operands or chunk descriptions that are not there.  Every
+// wait ends: those of the roles and those for loads and commits in flight, all
+// through mbar_wait_bounded, then the block's barrier, which every warp reaches.  The
+// products whose commit is left out were issued a second earlier, and the next commit
+// of the same thread, where there is one, covers them before tensor memory is freed.
 #include "lq_umma.cuh"
 
 namespace lq {
